@@ -117,6 +117,7 @@ def draw(rng):
 def _lens(case):
     r = random.Random(case["lens_seed"])
     ctx = [r.randint(case["lo"], case["hi"]) for _ in range(case["seqs"])]
+    ctx[0] = max(ctx[0], 1)
     if case["op"] != "prefill":
         return ctx, None
     if case["qhi"] == 0:            # whole prompts
@@ -196,6 +197,15 @@ def _store(cache, case, x, blk, off):
     _scales(cache, case)[blk, :, off] = (e + 127).to(torch.uint8)
 
 
+def _filled(case, x):
+    """A cache that holds the values x [blocks, Hkv, bs, D]."""
+    cache = _new_cache(case, x.shape[0])
+    codes, e = _quantise(x)
+    _codes(cache, case).copy_(codes.view(torch.uint8))
+    _scales(cache, case).copy_(e + 127)
+    return cache
+
+
 def _paged(case, gen):
     """A block table over a pool in random order, both caches filled, and the lengths."""
     ctx, qs = _lens(case)
@@ -211,16 +221,9 @@ def _paged(case, gen):
     st = dict(case=case, tables=tables, lens=L.to(torch.int32), L=L, ctx=ctx, qs=qs)
     # channel-dependent spread for keys, smaller values for V, as projections give
     spread = torch.exp(0.5 * torch.randn(case["head"], generator=gen, device="cuda"))
-    for name, scale in (("k_cache", spread), ("v_cache", torch.full_like(spread, 0.5))):
-        c = _new_cache(case, pool)
-        for at in range(0, pool, 256):
-            n = min(256, pool - at)
-            x = torch.randn((n, case["kv_heads"], bs, case["head"]), generator=gen, device="cuda") * scale
-            codes, e = _quantise(x)
-            _codes(c, case)[at:at + n] = codes.view(torch.uint8)
-            _scales(c, case)[at:at + n] = (e + 127).to(torch.uint8)
-        st[name] = c
-    st["spread"] = spread
+    shape = pool, case["kv_heads"], bs, case["head"]
+    st["k_cache"] = _filled(case, torch.randn(shape, generator=gen, device="cuda") * spread)
+    st["v_cache"] = _filled(case, torch.randn(shape, generator=gen, device="cuda") * 0.5)
     return st
 
 
@@ -251,13 +254,6 @@ def prepare(case, seed):
     if op == "decode":
         st["q"] = _randn(gen, (S, case["heads"], D), dt)
         st["out"] = torch.empty_like(st["q"])
-        if own:
-            import paged_kv_cache_480_b200 as pkv
-            code = {"f32": 0, "f16": 1, "bf16": 2}[case["dtype"]]
-            most = st["tables"].shape[1] * case["block"]
-            st["most"] = most
-            st["workspace"] = torch.zeros(pkv.paged_attention_workspace_size(
-                S, case["heads"], case["kv_heads"], D, case["block"], most, code), dtype=torch.uint8, device="cuda")
         return st
     counts = st["ctx"] if op == "read" else st["qs"]
     st["start"] = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
@@ -336,11 +332,11 @@ def _plain_write(st):
 def _written(st, q):
     """The caches as the values their bytes stand for: codes and scales."""
     c = st["case"]
-    out = {} if q is None else {"q": q}
-    for name in ("k_cache", "v_cache"):
-        out[name] = _codes(st[name], c).view(torch.float8_e4m3fn)
-        out[name + "_scales"] = _scales(st[name], c).view(torch.float8_e8m0fnu)
-    return out
+    return ({} if q is None else {"q": q}) | {
+        "k_cache": _codes(st["k_cache"], c).view(torch.float8_e4m3fn),
+        "k_cache_scales": _scales(st["k_cache"], c).view(torch.float8_e8m0fnu),
+        "v_cache": _codes(st["v_cache"], c).view(torch.float8_e4m3fn),
+        "v_cache_scales": _scales(st["v_cache"], c).view(torch.float8_e8m0fnu)}
 
 
 def _plain_read(st):
@@ -406,8 +402,7 @@ def _own(st):
         return {"k": st["k_out"], "v": st["v_out"]}
     if op == "decode":
         return pkv.paged_attention_decode_fp8row(st["out"], st["q"], st["k_cache"], st["v_cache"], st["tables"],
-                                                 st["lens"], scale, max_context_len=st["most"],
-                                                 workspace=st["workspace"])
+                                                 st["lens"], scale)
     return pkv.paged_attention_prefill_fp8row(st["out"], st["q"], st["k_cache"], st["v_cache"], st["tables"],
                                               st["lens"], st["start"], scale, max_query_len=st["most_q"])
 
