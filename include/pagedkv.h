@@ -207,6 +207,163 @@ pkv_status reshape_and_cache_fp8kv(const void* key, const void* value, void* k_c
                                   int64_t key_token_stride, int64_t value_token_stride,
                                   pkv_dtype dtype, float k_scale, float v_scale, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit row cache ("fp8row"): an E4M3 cache in which every row -- one token of
+ * one KV head -- has a power-of-two scale of its own, chosen when the row is
+ * written, so no scales are calibrated or passed around.
+ *
+ * Each cache is [num_blocks][num_kv_heads][block_size * (head_size + 1)]
+ * bytes: per (block, KV head) the block_size rows of head_size E4M3 codes,
+ * then the block_size rows' scale bytes.  A scale byte b stands for 2^(b -
+ * 127), a cache element for code * 2^(b - 127).  copy_blocks and swap_blocks
+ * move codes and scales together (block_bytes = num_kv_heads * block_size *
+ * (head_size + 1), a multiple of 16).
+ *
+ * reshape_and_cache_fp8row: reshape_and_cache into such caches.  A row x gets
+ * the smallest exponent e in [-60, 60] with max|x| <= 448 * 2^e, b = e + 127;
+ * each element becomes e4m3(x * 2^-e), rounded once to nearest even and
+ * saturating at +-448 (so +-infinity reads back as +-448 * 2^60).  A row that
+ * holds a NaN gets b = 255 and reads as NaN in every element.  key/value in
+ * `dtype`; strides and slots as in reshape_and_cache; a row and its scale
+ * byte are the only bytes written.  Two tokens of one call must not have the
+ * same slot.
+ *
+ * paged_attention_decode_fp8row: paged_attention_decode over such caches.  The
+ * softmax weights are taken relative to the largest weight times V scale, so
+ * rows of very different scales keep their precision.  With 16-bit q the
+ * products run on the tensor cores in fp16 (bf16 q is rounded to fp16 there,
+ * so |q| must stay below 65504).  Workspace, partitioning, checks and errors
+ * as for paged_attention_decode.
+ *
+ * Scale bytes the calls never write (below 67, 188 to 254) give undefined
+ * values, and codes 0x7f / 0xff occur only in NaN rows.
+ * Supported: head_size 64 or 128, block_size 16 or 32.
+ * ------------------------------------------------------------------------- */
+pkv_status reshape_and_cache_fp8row(const void* key, const void* value, void* k_cache, void* v_cache,
+                                    const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_size,
+                                    int block_size, int num_blocks, int64_t key_token_stride,
+                                    int64_t value_token_stride, pkv_dtype dtype, void* stream);
+
+pkv_status paged_attention_decode_fp8row(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                         int num_kv_heads, int block_size, int num_seqs, int num_heads, int head_size,
+                                         int num_blocks, int max_blocks_per_seq, int max_context_len, pkv_dtype dtype,
+                                         int partition_size, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * rotary_embedding rotates the first rotary_dim elements of every head of q
+ * and k by angles of the token's position: pair i < rotary_dim / 2 by a = p *
+ * inv_freq[i],
+ *   (x, y) -> attention_scale * (x cos a - y sin a, y cos a + x sin a),
+ * a pair being elements (2i, 2i + 1) if interleaved, else (i, i + rotary_dim /
+ * 2).  The other elements are copied.  Angles are formed and reduced in fp64,
+ * the rotation is fp32 with one rounding at the end, so positions of any size
+ * are as exact as near ones.
+ *
+ *   q_out, k_out   device, token t's head h at element t * *_token_stride + h *
+ *                  head_size (written); may be q and k themselves with the
+ *                  same strides, but must not overlap them in any other way
+ *   q, k           device, dtype; num_heads or num_kv_heads 0: no q or no k
+ *                  (pointers not looked at)
+ *   positions      device, int64 [num_tokens]
+ *   inv_freq       device, float [rotary_dim / 2] (pkv_rotary_frequencies)
+ *   rotary_dim     even, 2 .. head_size
+ *   strides        in elements, multiples of 16 bytes, at least a token's rows
+ * Supported: dtype f32/f16/bf16, head_size a multiple of 16 up to 512.
+ *
+ * rotary_reshape_and_cache: q as above; k is rotated and written, with value,
+ * to its slot (reshape_and_cache of the rotated key, in one launch; a negative
+ * slot means no cache write, q is rotated all the same).
+ * rotary_reshape_and_cache_fp8row: the same into an 8-bit row cache; the
+ * rotated key stays in fp32 until its one rounding to E4M3.
+ * Supported by both: head_size 64 or 128, block_size 16 or 32; num_heads may
+ * be 0.  Two tokens of one call must not have the same slot.
+ * ------------------------------------------------------------------------- */
+pkv_status rotary_embedding(void* q_out, void* k_out, const void* q, const void* k, const int64_t* positions,
+                            const float* inv_freq, int num_tokens, int num_heads, int num_kv_heads, int head_size,
+                            int rotary_dim, int interleaved, float attention_scale, int64_t q_out_token_stride,
+                            int64_t k_out_token_stride, int64_t q_token_stride, int64_t k_token_stride,
+                            pkv_dtype dtype, void* stream);
+
+pkv_status rotary_reshape_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                                    void* v_cache, const int64_t* positions, const int64_t* slot_mapping,
+                                    const float* inv_freq, int num_tokens, int num_heads, int num_kv_heads,
+                                    int head_size, int rotary_dim, int interleaved, float attention_scale,
+                                    int block_size, int num_blocks, int64_t q_out_token_stride,
+                                    int64_t q_token_stride, int64_t key_token_stride, int64_t value_token_stride,
+                                    pkv_dtype dtype, void* stream);
+
+pkv_status rotary_reshape_and_cache_fp8row(void* q_out, const void* q, const void* key, const void* value,
+                                           void* k_cache, void* v_cache, const int64_t* positions,
+                                           const int64_t* slot_mapping, const float* inv_freq, int num_tokens,
+                                           int num_heads, int num_kv_heads, int head_size, int rotary_dim,
+                                           int interleaved, float attention_scale, int block_size, int num_blocks,
+                                           int64_t q_out_token_stride, int64_t q_token_stride,
+                                           int64_t key_token_stride, int64_t value_token_stride, pkv_dtype dtype,
+                                           void* stream);
+
+/* Host table of rotary frequencies: inv_freq[i] = base^(-2i / rotary_dim),
+ * i < rotary_dim / 2 (host memory), computed in double and rounded once, and
+ * stretched for contexts `factor` (>= 1) times longer than original_context:
+ *   PLAIN      as they are (factor, original_context and turns not looked at)
+ *   LINEAR     all divided by factor
+ *   BASE       base multiplied by factor^(R / (R - 2)), R = rotary_dim: the
+ *              slowest pair is divided by factor, the fastest kept
+ *   BY_TURNS   pairs that make more than fast_turns turns over the original
+ *              context are kept, those with fewer than slow_turns divided by
+ *              factor, between them a blend that is linear in the turns
+ *   BY_INDEX   the same two bounds, the blend linear in the pair's index
+ *              (between the whole indices around them), and *attention_scale
+ *              = 0.1 ln(factor) + 1
+ * *attention_scale (host) is 1 for the others. */
+typedef enum {
+    PKV_ROTARY_PLAIN = 0,
+    PKV_ROTARY_LINEAR = 1,
+    PKV_ROTARY_BASE = 2,
+    PKV_ROTARY_BY_TURNS = 3,
+    PKV_ROTARY_BY_INDEX = 4
+} pkv_rotary_scaling;
+
+pkv_status pkv_rotary_frequencies(float* inv_freq, float* attention_scale, int rotary_dim, double base,
+                                  pkv_rotary_scaling scaling, double factor, int64_t original_context,
+                                  double fast_turns, double slow_turns);
+
+/* ---------------------------------------------------------------------------
+ * gather_cache -- read whole sequences back out of the pages.
+ *
+ * Defines: row start_loc[s] + t of k_out is token t of sequence s (block
+ * block_tables[s][t / bs], offset t % bs), for t < start_loc[s + 1] -
+ * start_loc[s]; likewise v_out.  gather_cache copies bits, gather_cache_fp8kv
+ * gives code * k_scale (v_scale) and gather_cache_fp8row code * 2^(b - 127),
+ * taken in fp32 and rounded once to `dtype` (beyond fp16's range: infinity).
+ *
+ *   k_out, v_out   device, [num_tokens][num_kv_heads][head_size], dtype; rows
+ *                  outside [start_loc[0], start_loc[num_seqs]) stay as they are
+ *   start_loc      device, int32 [num_seqs + 1], non-decreasing
+ *   num_tokens     rows of k_out and v_out, >= start_loc[num_seqs]
+ * Device checks: a token past max_blocks_per_seq blocks sets
+ * PKV_DEVERR_CONTEXT and is not written; a block id outside the pool sets
+ * PKV_DEVERR_BLOCK_ID and its rows read as zeros.
+ * Supported: dtype f32/f16/bf16 (the caches' type for gather_cache), head_size
+ * 64 or 128, block_size 16 or 32.
+ * ------------------------------------------------------------------------- */
+pkv_status gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, const int32_t* start_loc, int num_tokens, int num_seqs,
+                        int num_kv_heads, int head_size, int block_size, int num_blocks, int max_blocks_per_seq,
+                        pkv_dtype dtype, void* stream);
+
+pkv_status gather_cache_fp8kv(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* start_loc, float k_scale, float v_scale,
+                              int num_tokens, int num_seqs, int num_kv_heads, int head_size, int block_size,
+                              int num_blocks, int max_blocks_per_seq, pkv_dtype dtype, void* stream);
+
+pkv_status gather_cache_fp8row(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, const int32_t* start_loc, int num_tokens, int num_seqs,
+                               int num_kv_heads, int head_size, int block_size, int num_blocks,
+                               int max_blocks_per_seq, pkv_dtype dtype, void* stream);
+
 /* Bytes of workspace paged_attention_decode needs for these sizes (0 on bad
  * arguments).  partition_size as in paged_attention_decode. */
 size_t paged_attention_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
@@ -391,6 +548,26 @@ pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache
                                    int num_kv_heads, int head_size, int block_size,
                                    int num_blocks, int max_blocks_per_seq, int max_query_len,
                                    pkv_dtype dtype, void* stream);
+
+/* paged_attention_prefill over an E4M3 cache (one scale for all of K and one
+ * for all of V, as in paged_attention_decode_fp8kv) and over an 8-bit row
+ * cache: every argument, check and error as there, the caches as described
+ * with those formats.  Each cache element is taken in q's type: exact in bf16
+ * and within fp16's range; with f16 q an element of a row cache beyond +-65504
+ * becomes infinity and one below 2^-24 rounds to a multiple of 2^-24. */
+pkv_status paged_attention_prefill_fp8kv(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* context_lens,
+                                         const int32_t* query_start_loc, float scale, float k_scale, float v_scale,
+                                         int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                         int block_size, int num_blocks, int max_blocks_per_seq, int max_query_len,
+                                         pkv_dtype dtype, void* stream);
+
+pkv_status paged_attention_prefill_fp8row(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* query_start_loc, float scale, int num_tokens, int num_seqs,
+                                          int num_heads, int num_kv_heads, int head_size, int block_size,
+                                          int num_blocks, int max_blocks_per_seq, int max_query_len, pkv_dtype dtype,
+                                          void* stream);
 
 /* Synchronise the stream, return the sticky device-check bits of the
  * current device in *bits and clear them.  Returns PKV_ERR_DEVICE_CHECK if

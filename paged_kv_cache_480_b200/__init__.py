@@ -17,6 +17,10 @@ __all__ = [
     "paged_attention_decode_noalloc", "paged_attention_prefill",
     "reshape_and_cache_fp8kv", "paged_attention_workspace_size", "paged_attention_partition_size",
     "reshape_and_cache", "copy_blocks", "swap_blocks", "read_device_errors", "set_wait_limit", "BlockManager",
+    "fp8row_cache_shape", "reshape_and_cache_fp8row", "paged_attention_decode_fp8row",
+    "paged_attention_prefill_fp8row", "paged_attention_prefill_fp8kv",
+    "rotary_frequencies", "rotary_embedding", "rotary_reshape_and_cache", "rotary_reshape_and_cache_fp8row",
+    "gather_cache", "gather_cache_fp8kv", "gather_cache_fp8row",
     "load_library",
     "PagedKVError", "OutOfBlocks", "default_workspace",
 ]

@@ -76,6 +76,24 @@ def load_library(path=LIB_PATH):
         lib.reshape_and_cache_fp8kv.restype = I
         lib.paged_attention_prefill.argtypes = [P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, P]
         lib.paged_attention_prefill.restype = I
+        lib.reshape_and_cache_fp8row.argtypes = [P, P, P, P, P, I, I, I, I, I, I64, I64, I, P]
+        lib.paged_attention_decode_fp8row.argtypes = [P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, P, SZ, P]
+        lib.paged_attention_prefill_fp8row.argtypes = [P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, P]
+        lib.paged_attention_prefill_fp8kv.argtypes = [P, P, P, P, P, P, P, F, F, F, I, I, I, I, I, I, I, I, I, I, P]
+        lib.rotary_embedding.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, I64, I64, I64, I64, I, P]
+        lib.rotary_reshape_and_cache.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I64, I64, I64,
+                                                 I64, I, P]
+        lib.rotary_reshape_and_cache_fp8row.argtypes = lib.rotary_reshape_and_cache.argtypes
+        lib.pkv_rotary_frequencies.argtypes = [P, P, I, ctypes.c_double, I, ctypes.c_double, I64, ctypes.c_double,
+                                               ctypes.c_double]
+        lib.gather_cache.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]
+        lib.gather_cache_fp8row.argtypes = lib.gather_cache.argtypes
+        lib.gather_cache_fp8kv.argtypes = [P, P, P, P, P, P, F, F, I, I, I, I, I, I, I, I, P]
+        for name in ("reshape_and_cache_fp8row", "paged_attention_decode_fp8row", "paged_attention_prefill_fp8row",
+                     "paged_attention_prefill_fp8kv", "rotary_embedding", "rotary_reshape_and_cache",
+                     "rotary_reshape_and_cache_fp8row", "pkv_rotary_frequencies", "gather_cache",
+                     "gather_cache_fp8row", "gather_cache_fp8kv"):
+            getattr(lib, name).restype = I
         lib.pkv_read_device_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
         lib.pkv_read_device_errors.restype = I
         lib.pkv_set_wait_limit.argtypes = [I64]
@@ -347,6 +365,304 @@ def reshape_and_cache_fp8kv(key, value, k_cache, v_cache, slot_mapping, k_scale,
         key.stride(0), value.stride(0), _dtype_code(key), float(k_scale), float(v_scale),
         _stream(stream, key.device))
     _check(st, "reshape_and_cache_fp8kv")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit row cache: E4M3 codes with one power-of-two scale a row
+# ---------------------------------------------------------------------------
+def fp8row_cache_shape(num_blocks, num_kv_heads, block_size, head_size):
+    """Shape of a uint8 row cache: per (block, KV head) block_size rows of
+    head_size codes, then block_size scale bytes."""
+    return num_blocks, num_kv_heads, block_size * (head_size + 1)
+
+
+def _row_caches(k_cache, v_cache, D):
+    """(num_blocks, num_kv_heads, block_size) of a pair of row caches."""
+    import torch
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+        raise TypeError("row caches are uint8 (fp8row_cache_shape)")
+    NB, Hkv, n = k_cache.shape
+    if v_cache.shape != k_cache.shape or n % (D + 1):
+        raise ValueError("row caches must be [num_blocks, num_kv_heads, block_size * (head_size + 1)]")
+    return NB, Hkv, n // (D + 1)
+
+
+def _rows(t, name):
+    """Device pointer of [T, heads, head_size] rows whose tokens may lie apart, and their stride."""
+    if t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name}: heads must be contiguous within a token")
+    # (a single token's stride may be anything: it is never applied)
+    return _cuda(t, name), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _int64(t, n, name):
+    import torch
+    if t.dtype != torch.int64 or t.numel() != n:
+        raise TypeError(f"{name} must be int64 [{n}]")
+    return _contig(t, name)
+
+
+def reshape_and_cache_fp8row(key, value, k_cache, v_cache, slot_mapping, stream=None):
+    """Quantising cache write into 8-bit row caches (reshape_and_cache_fp8row in
+    pagedkv.h): key/value [T, Hkv, D] in f32/f16/bf16, each (token, head) row
+    with a scale of its own."""
+    lib = load_library()
+    T, Hkv, D = key.shape
+    NB, Hkv2, bs = _row_caches(k_cache, v_cache, D)
+    if Hkv != Hkv2 or value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError("key/value shape does not match the cache")
+    _same_device(key, value, k_cache, v_cache, slot_mapping)
+    kp, ks = _rows(key, "key")
+    vp, vs = _rows(value, "value")
+    st = lib.reshape_and_cache_fp8row(kp, vp, _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
+                                      _int64(slot_mapping, T, "slot_mapping"), T, Hkv, D, bs, NB, ks, vs,
+                                      _dtype_code(key), _stream(stream, key.device))
+    _check(st, "reshape_and_cache_fp8row")
+
+
+def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len=None,
+                                  partition_size=0, workspace=None, stream=None):
+    """Decode attention over 8-bit row caches (paged_attention_decode_fp8row in
+    pagedkv.h): q, out [S, H, D] in f32/f16/bf16; caches of fp8row_cache_shape."""
+    import torch
+    lib = load_library()
+    S, H, D = q.shape
+    NB, Hkv, bs = _row_caches(k_cache, v_cache, D)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out and q must share shape and dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if block_tables.shape[0] != S or context_lens.numel() != S:
+        raise ValueError("block_tables must be [S, MB] and context_lens [S]")
+    _same_device(q, out, k_cache, v_cache, block_tables, context_lens)
+    MB = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = MB * bs
+    code = _dtype_code(q)
+    need = lib.paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
+    if need == 0:
+        raise PagedKVError(2, "paged_attention_workspace_size")
+    if workspace is None:
+        workspace = default_workspace(q.device, need)
+    st = lib.paged_attention_decode_fp8row(
+        _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
+        _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"), float(scale), Hkv, bs, S, H, D,
+        NB, MB, int(max_context_len), code, int(partition_size), _cuda(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream, q.device))
+    _check(st, "paged_attention_decode_fp8row")
+    return out
+
+
+def _prefill_args(out, q, block_tables, context_lens, query_start_loc, max_query_len):
+    import torch
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out and q must share shape and dtype")
+    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
+            or query_start_loc.dtype != torch.int32):
+        raise TypeError("block_tables, context_lens and query_start_loc must be int32")
+    S = context_lens.numel()
+    if query_start_loc.numel() != S + 1 or block_tables.shape[0] != S:
+        raise ValueError("query_start_loc must be [S + 1] and block_tables [S, MB]")
+    if max_query_len is None:
+        raise ValueError("max_query_len is required (a host-known bound of the queries per sequence)")
+    return S
+
+
+def paged_attention_prefill_fp8row(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                   max_query_len=None, stream=None):
+    """Causal attention of prompts or chunks over 8-bit row caches
+    (paged_attention_prefill_fp8row in pagedkv.h); arguments as for
+    paged_attention_prefill, caches of fp8row_cache_shape."""
+    lib = load_library()
+    T, H, D = q.shape
+    NB, Hkv, bs = _row_caches(k_cache, v_cache, D)
+    S = _prefill_args(out, q, block_tables, context_lens, query_start_loc, max_query_len)
+    _same_device(q, out, k_cache, v_cache, block_tables, context_lens, query_start_loc)
+    st = lib.paged_attention_prefill_fp8row(
+        _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
+        _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"),
+        _contig(query_start_loc, "query_start_loc"), float(scale), T, S, H, Hkv, D, bs, NB,
+        block_tables.shape[1], int(max_query_len), _dtype_code(q), _stream(stream, q.device))
+    _check(st, "paged_attention_prefill_fp8row")
+    return out
+
+
+def paged_attention_prefill_fp8kv(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                  k_scale, v_scale, max_query_len=None, stream=None):
+    """Causal attention of prompts or chunks over FP8 E4M3 caches with one scale
+    for K and one for V (paged_attention_prefill_fp8kv in pagedkv.h):
+    k_cache / v_cache uint8 [NB, Hkv, bs, D]."""
+    lib = load_library()
+    T, H, D = q.shape
+    NB, Hkv, bs, D2 = k_cache.shape
+    if D2 != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch")
+    S = _prefill_args(out, q, block_tables, context_lens, query_start_loc, max_query_len)
+    _same_device(q, out, k_cache, v_cache, block_tables, context_lens, query_start_loc)
+    st = lib.paged_attention_prefill_fp8kv(
+        _contig(out, "out"), _contig(q, "q"), _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache"),
+        _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"),
+        _contig(query_start_loc, "query_start_loc"), float(scale), float(k_scale), float(v_scale), T, S, H, Hkv, D,
+        bs, NB, block_tables.shape[1], int(max_query_len), _dtype_code(q), _stream(stream, q.device))
+    _check(st, "paged_attention_prefill_fp8kv")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+ROTARY_SCALING = {None: 0, "linear": 1, "base": 2, "by_turns": 3, "by_index": 4}
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_context=0, fast_turns=32.0,
+                       slow_turns=1.0):
+    """(inv_freq, attention_scale) of pkv_rotary_frequencies in pagedkv.h:
+    inv_freq float32 [rotary_dim / 2] on the host, to be moved to the device
+    once; scaling None, "linear", "base", "by_turns" or "by_index"."""
+    import torch
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {list(ROTARY_SCALING)}")
+    inv_freq = torch.empty(max(int(rotary_dim), 2) // 2, dtype=torch.float32)
+    att = ctypes.c_float()
+    st = load_library().pkv_rotary_frequencies(ctypes.c_void_p(inv_freq.data_ptr()), ctypes.byref(att),
+                                               int(rotary_dim), float(base), ROTARY_SCALING[scaling], float(factor),
+                                               int(original_context), float(fast_turns), float(slow_turns))
+    _check(st, "pkv_rotary_frequencies")
+    return inv_freq, att.value
+
+
+def _inv_freq(t, D):
+    import torch
+    if t.dtype != torch.float32 or t.dim() != 1 or not 1 <= t.numel() <= D // 2:
+        raise TypeError("inv_freq must be float32 [rotary_dim / 2] with rotary_dim <= head_size")
+    return _contig(t, "inv_freq")
+
+
+def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, interleaved=False, attention_scale=1.0, stream=None):
+    """Rotary positions of q [T, H, D] and k [T, Hkv, D] (rotary_embedding in
+    pagedkv.h).  q_out / k_out may be q / k; k and k_out may be None.
+    positions: int64 [T]; inv_freq: float32 [rotary_dim / 2] on the device."""
+    lib = load_library()
+    T, H, D = q.shape
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    pairs = [(q_out, q, "q")] + ([] if k is None else [(k_out, k, "k")])
+    for o, x, name in pairs:
+        if o.shape != x.shape or o.dtype != q.dtype or x.dtype != q.dtype or x.shape[0] != T or x.shape[2] != D:
+            raise ValueError(f"{name} and {name}_out must be [T, heads, head_size] of q's dtype")
+        if o.data_ptr() == x.data_ptr() and T > 1 and o.stride(0) != x.stride(0):
+            raise ValueError(f"{name}_out in place of {name} must have its strides")
+        _same_device(q, o, x)
+    _same_device(q, positions, inv_freq)
+    qp, qs = _rows(q, "q")
+    qop, qos = _rows(q_out, "q_out")
+    kp, ks = (None, 0) if k is None else _rows(k, "k")
+    kop, kos = (None, 0) if k is None else _rows(k_out, "k_out")
+    st = lib.rotary_embedding(qop, kop, qp, kp, _int64(positions, T, "positions"), _inv_freq(inv_freq, D), T, H,
+                              0 if k is None else k.shape[1], D, 2 * inv_freq.numel(), int(bool(interleaved)),
+                              float(attention_scale), qos, kos, qs, ks, _dtype_code(q), _stream(stream, q.device))
+    _check(st, "rotary_embedding")
+
+
+def _rotary_write(name, q_out, q, key, value, k_cache, v_cache, NB, Hkv, bs, positions, slot_mapping, inv_freq,
+                  interleaved, attention_scale, stream):
+    lib = load_library()
+    T, H, D = q.shape
+    if q_out.shape != q.shape or tuple(key.shape) != (T, Hkv, D) or value.shape != key.shape:
+        raise ValueError("q, q_out, key and value must be [T, heads, head_size] and match the caches")
+    if q_out.dtype != q.dtype or key.dtype != q.dtype or value.dtype != q.dtype:
+        raise ValueError("q, q_out, key and value must share a dtype")
+    if q_out.data_ptr() == q.data_ptr() and T > 1 and q_out.stride(0) != q.stride(0):
+        raise ValueError("q_out in place of q must have its strides")
+    _same_device(q, q_out, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq)
+    qp, qs = _rows(q, "q")
+    qop, qos = _rows(q_out, "q_out")
+    kp, ks = _rows(key, "key")
+    vp, vs = _rows(value, "value")
+    st = getattr(lib, name)(qop, qp, kp, vp, _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
+                            _int64(positions, T, "positions"), _int64(slot_mapping, T, "slot_mapping"),
+                            _inv_freq(inv_freq, D), T, H, Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)),
+                            float(attention_scale), bs, NB, qos, qs, ks, vs, _dtype_code(q),
+                            _stream(stream, q.device))
+    _check(st, name)
+    return q_out
+
+
+def rotary_reshape_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
+                             interleaved=False, attention_scale=1.0, stream=None):
+    """Rotary positions of q, and of key on its way into the cache with value
+    (rotary_reshape_and_cache in pagedkv.h).  q_out may be q."""
+    NB, Hkv, bs, D = k_cache.shape
+    if D != q.shape[2] or v_cache.shape != k_cache.shape or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size] of q's dtype")
+    return _rotary_write("rotary_reshape_and_cache", q_out, q, key, value, k_cache, v_cache, NB, Hkv, bs, positions,
+                         slot_mapping, inv_freq, interleaved, attention_scale, stream)
+
+
+def rotary_reshape_and_cache_fp8row(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
+                                    interleaved=False, attention_scale=1.0, stream=None):
+    """rotary_reshape_and_cache into 8-bit row caches
+    (rotary_reshape_and_cache_fp8row in pagedkv.h)."""
+    NB, Hkv, bs = _row_caches(k_cache, v_cache, q.shape[2])
+    return _rotary_write("rotary_reshape_and_cache_fp8row", q_out, q, key, value, k_cache, v_cache, NB, Hkv, bs,
+                         positions, slot_mapping, inv_freq, interleaved, attention_scale, stream)
+
+
+# ---------------------------------------------------------------------------
+# reading sequences back
+# ---------------------------------------------------------------------------
+def _gather(name, k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc, scales, stream):
+    import torch
+    lib = load_library()
+    T, Hkv2, D = k_out.shape
+    if Hkv2 != Hkv or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out must be [T, num_kv_heads, head_size] and match the caches")
+    if block_tables.dtype != torch.int32 or start_loc.dtype != torch.int32:
+        raise TypeError("block_tables and start_loc must be int32")
+    S, MB = block_tables.shape
+    if start_loc.numel() != S + 1:
+        raise ValueError("start_loc must be [S + 1]")
+    _same_device(k_out, v_out, k_cache, v_cache, block_tables, start_loc)
+    st = getattr(lib, name)(_contig(k_out, "k_out"), _contig(v_out, "v_out"), _contig(k_cache, "k_cache"),
+                            _contig(v_cache, "v_cache"), _contig(block_tables, "block_tables"),
+                            _contig(start_loc, "start_loc"), *scales, T, S, Hkv, D, bs, NB, MB, _dtype_code(k_out),
+                            _stream(stream, k_out.device))
+    _check(st, name)
+    return k_out, v_out
+
+
+def gather_cache(k_out, v_out, k_cache, v_cache, block_tables, start_loc, stream=None):
+    """Sequences read back from the pages (gather_cache in pagedkv.h): token t of
+    sequence s goes to row start_loc[s] + t of k_out and v_out [T, Hkv, D]."""
+    NB, Hkv, bs, D = k_cache.shape
+    if D != k_out.shape[2] or v_cache.shape != k_cache.shape or k_cache.dtype != k_out.dtype \
+            or v_cache.dtype != k_out.dtype:
+        raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size] of k_out's dtype")
+    return _gather("gather_cache", k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc, (), stream)
+
+
+def gather_cache_fp8kv(k_out, v_out, k_cache, v_cache, block_tables, start_loc, k_scale, v_scale, stream=None):
+    """gather_cache out of FP8 E4M3 caches with one scale for K and one for V."""
+    NB, Hkv, bs, D = k_cache.shape
+    if D != k_out.shape[2] or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
+    _fp8_cache(k_cache, "k_cache")
+    _fp8_cache(v_cache, "v_cache")
+    return _gather("gather_cache_fp8kv", k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc,
+                   (float(k_scale), float(v_scale)), stream)
+
+
+def gather_cache_fp8row(k_out, v_out, k_cache, v_cache, block_tables, start_loc, stream=None):
+    """gather_cache out of 8-bit row caches; k_out, v_out in f32/f16/bf16."""
+    NB, Hkv, bs = _row_caches(k_cache, v_cache, k_out.shape[2])
+    return _gather("gather_cache_fp8row", k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc, (),
+                   stream)
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "fp8row.cuh"
 
 namespace pkv {
 
@@ -79,7 +80,8 @@ template <typename TQ, typename TC, int D, int BS, int G>
 struct DecodeShape {
     static constexpr int EPC = Elem<TC>::kPerChunk;  // cache elements per 16-byte chunk
     static constexpr int ROW = D * (int)sizeof(TC);  // bytes per cache token row
-    static constexpr int TILE = BS * ROW;            // bytes per (block, KV head) tile
+    static constexpr int TILE = cache_tile_bytes<TC>(D, BS);   // bytes per (block, KV head) tile
+    static constexpr int SCALES = BS * ROW;          // row-scaled cache: the tile's scale bytes
     static constexpr int QROW = D * (int)sizeof(TQ); // bytes per q / out row
     static constexpr int QBYTES = G * QROW;          // q rows of one item, at most
 };
@@ -205,6 +207,7 @@ struct FmaConsumer {
 
     __device__ __forceinline__ void block(const unsigned char* Kt, const unsigned char* Vt,
                                           int nvalid, float) {
+        constexpr bool kRow = kRowScaled<TC>;
         float z[NSTEP];
 #pragma unroll
         for (int i = 0; i < NSTEP; ++i) {
@@ -224,6 +227,9 @@ struct FmaConsumer {
             float sc = s0 + s1;
 #pragma unroll
             for (int off = 1; off < Q; off <<= 1) sc += __shfl_xor_sync(kFull, sc, off);
+            // row scales: see MmaConsumerFp8
+            if constexpr (kRow)
+                sc = fmaf(sc, row_scale(Kt[S::SCALES + t]), row_exponent(Vt[S::SCALES + t]));
             z[i] = (t < nvalid) ? sc : -INFINITY;
         }
         float mb = z[0];
@@ -241,7 +247,8 @@ struct FmaConsumer {
             const int t = i * TS + u;
             if (t < nvalid) {
                 const float pr = ex2(z[i] - m_new);
-                l_run += pr;
+                if constexpr (kRow) l_run = fmaf(pr, row_scale_inv(Vt[S::SCALES + t]), l_run);
+                else l_run += pr;
                 const uint4* row = reinterpret_cast<const uint4*>(Vt + t * S::ROW);
 #pragma unroll
                 for (int k = 0; k < CPL; ++k) {
@@ -517,10 +524,21 @@ struct MmaConsumer {
 // V^T pairs of adjacent tokens are gathered byte-wise with permutes, then
 // converted pairwise.  The per-tensor scales enter the logits (k_scale) and
 // the output (v_scale).
+//
+// Row scales (fp8row): token t has exponents ek and ev of its K and V rows.
+// What it adds to the output is 2^(z + ev) * code with z its logit in log2
+// units, so y = z + ev takes the logit's place: the running maximum m is of y,
+// the weights w = 2^(y - m) are what is rounded to fp16 for the PV product
+// (the largest contributions keep full precision, whatever the spread of the
+// scales), and the softmax sum takes w * 2^-ev in fp32.  Output, partial sums
+// and merge then have the form they have without scales: sum(w code) / sum(w
+// 2^-ev), both relative to m.  Costs two byte loads and three operations a
+// token and head column.
 // ===========================================================================
-template <typename TQ, int D, int BS, int G>
+template <typename TQ, typename TC, int D, int BS, int G>
 struct MmaConsumerFp8 {
-    using S = DecodeShape<TQ, fp8e4m3, D, BS, G>;
+    using S = DecodeShape<TQ, TC, D, BS, G>;
+    static constexpr bool kRow = kRowScaled<TC>;
     static_assert(sizeof(TQ) == 2, "q must be 16-bit");
     static_assert(G <= 8, "the 8 MMA columns hold the query heads of one group");
     static_assert(D % 64 == 0, "head_size 64 or 128");
@@ -612,10 +630,34 @@ struct MmaConsumerFp8 {
         }
     }
 
-    // Logits of a slice in log2 units; tokens at or past nvalid are -inf.
-    __device__ __forceinline__ void logits(const float (&sc)[4], int nvalid, float scale_log2,
+    // Scale bytes of the lane's two tokens of a slice (tokens past nvalid may
+    // hold anything: they read as scale 1).
+    struct RowScales {
+        int k0, k8, v0, v8;
+    };
+    __device__ __forceinline__ RowScales scales(const unsigned char* Ks, const unsigned char* Vs, int nvalid) const {
+        RowScales x{127, 127, 127, 127};
+        if constexpr (kRow) {
+            if (r < nvalid) { x.k0 = Ks[r]; x.v0 = Vs[r]; }
+            if (r + 8 < nvalid) { x.k8 = Ks[r + 8]; x.v8 = Vs[r + 8]; }
+        }
+        return x;
+    }
+
+    // Logits of a slice in log2 units (row scales: y); tokens at or past nvalid
+    // are -inf.
+    __device__ __forceinline__ void logits(const float (&sc)[4], int nvalid, float scale_log2, const RowScales& rs,
                                            float (&z)[4]) const {
         const bool v0 = r < nvalid, v8 = r + 8 < nvalid;
+        if constexpr (kRow) {
+            const float a = scale_log2 * row_scale(rs.k0), b = scale_log2 * row_scale(rs.k8);
+            const float ya = row_exponent(rs.v0), yb = row_exponent(rs.v8);
+            z[0] = v0 ? fmaf(sc[0], a, ya) : -INFINITY;
+            z[1] = v0 ? fmaf(sc[1], a, ya) : -INFINITY;
+            z[2] = v8 ? fmaf(sc[2], b, yb) : -INFINITY;
+            z[3] = v8 ? fmaf(sc[3], b, yb) : -INFINITY;
+            return;
+        }
         z[0] = v0 ? sc[0] * scale_log2 : -INFINITY;
         z[1] = v0 ? sc[1] * scale_log2 : -INFINITY;
         z[2] = v8 ? sc[2] * scale_log2 : -INFINITY;
@@ -624,12 +666,21 @@ struct MmaConsumerFp8 {
 
     // Weights of a slice against the new maxima (fp16 pairs), added to l, and
     // moved to the B-fragment layout of the PV products.
-    __device__ __forceinline__ void weights(const float (&z)[4], float n0, float n1, float& s0, float& s1,
-                                            uint32_t& pb0, uint32_t& pb1) const {
-        const uint32_t pk_lo = Elem<__half>::pack2(ex2(z[0] - n0), ex2(z[1] - n1));
-        const uint32_t pk_hi = Elem<__half>::pack2(ex2(z[2] - n0), ex2(z[3] - n1));
-        s0 += lo_f(pk_lo) + lo_f(pk_hi);
-        s1 += hi_f(pk_lo) + hi_f(pk_hi);
+    __device__ __forceinline__ void weights(const float (&z)[4], float n0, float n1, const RowScales& rs, float& s0,
+                                            float& s1, uint32_t& pb0, uint32_t& pb1) const {
+        const float p0 = ex2(z[0] - n0), p1 = ex2(z[1] - n1), p2 = ex2(z[2] - n0), p3 = ex2(z[3] - n1);
+        const uint32_t pk_lo = Elem<__half>::pack2(p0, p1);
+        const uint32_t pk_hi = Elem<__half>::pack2(p2, p3);
+        if constexpr (kRow) {
+            // from the unrounded weights: a row of a small scale may have a weight
+            // below fp16's range and still most of the softmax sum
+            const float ia = row_scale_inv(rs.v0), ib = row_scale_inv(rs.v8);
+            s0 = fmaf(p0, ia, fmaf(p2, ib, s0));
+            s1 = fmaf(p1, ia, fmaf(p3, ib, s1));
+        } else {
+            s0 += lo_f(pk_lo) + lo_f(pk_hi);
+            s1 += hi_f(pk_lo) + hi_f(pk_hi);
+        }
         const int src0 = (2 * c) * 4 + (r >> 1), src1 = src0 + 4;
         const uint32_t sel = (r & 1) ? 0x7632u : 0x5410u;
         const uint32_t x0 = __shfl_sync(kFull, pk_lo, src0), x1 = __shfl_sync(kFull, pk_lo, src1);
@@ -693,15 +744,17 @@ struct MmaConsumerFp8 {
         }
     }
 
-    __device__ __forceinline__ void slice(const unsigned char* Kt, const unsigned char* Vt,
-                                          int nvalid, float scale_log2) {
+    // Ks, Vs: the slice's scale bytes (row scales only)
+    __device__ __forceinline__ void slice(const unsigned char* Kt, const unsigned char* Vt, const unsigned char* Ks,
+                                          const unsigned char* Vs, int nvalid, float scale_log2) {
         float sc[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
+        const RowScales rs = scales(Ks, Vs, nvalid);
         qk(Kt, sc);
-        logits(sc, nvalid, scale_log2, z);
+        logits(sc, nvalid, scale_log2, rs, z);
         float n0, n1;
         update_max(fmaxf(z[0], z[2]), fmaxf(z[1], z[3]), n0, n1);
         uint32_t pb0, pb1;
-        weights(z, n0, n1, l0, l1, pb0, pb1);
+        weights(z, n0, n1, rs, l0, l1, pb0, pb1);
         pv(Vt, nvalid, pb0, pb1);
     }
 
@@ -710,18 +763,20 @@ struct MmaConsumerFp8 {
     // of the warp.
     __device__ __forceinline__ void slice2(const unsigned char* Ka, const unsigned char* Va, int nva,
                                            const unsigned char* Kb, const unsigned char* Vb, int nvb,
-                                           float scale_log2) {
+                                           const unsigned char* Ksa, const unsigned char* Vsa,
+                                           const unsigned char* Ksb, const unsigned char* Vsb, float scale_log2) {
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f}, za[4], zb[4];
+        const RowScales ra = scales(Ksa, Vsa, nva), rb = scales(Ksb, Vsb, nvb);
         qk(Ka, sa);
         qk(Kb, sb);
-        logits(sa, nva, scale_log2, za);
-        logits(sb, nvb, scale_log2, zb);
+        logits(sa, nva, scale_log2, ra, za);
+        logits(sb, nvb, scale_log2, rb, zb);
         float n0, n1;
         update_max(fmaxf(fmaxf(za[0], za[2]), fmaxf(zb[0], zb[2])), fmaxf(fmaxf(za[1], za[3]), fmaxf(zb[1], zb[3])),
                    n0, n1);
         uint32_t pa0, pa1, pb0, pb1;
-        weights(za, n0, n1, l0, l1, pa0, pa1);
-        weights(zb, n0, n1, l0, l1, pb0, pb1);
+        weights(za, n0, n1, ra, l0, l1, pa0, pa1);
+        weights(zb, n0, n1, rb, l0, l1, pb0, pb1);
         pv(Va, nva, pa0, pa1);
         pv(Vb, nvb, pb0, pb1);
     }
@@ -736,22 +791,24 @@ struct MmaConsumerFp8 {
 
     __device__ __forceinline__ void block(const unsigned char* Kt, const unsigned char* Vt,
                                           int nvalid, float scale_log2) {
+        const unsigned char* Ks = Kt + S::SCALES;
+        const unsigned char* Vs = Vt + S::SCALES;
         if (BS == 32 && kPairSlices && nvalid > 16) {
-            slice2(Kt, Vt, 16, Kt + 16 * S::ROW, Vt + 16 * S::ROW, nvalid - 16, scale_log2);
+            slice2(Kt, Vt, 16, Kt + 16 * S::ROW, Vt + 16 * S::ROW, nvalid - 16, Ks, Vs, Ks + 16, Vs + 16, scale_log2);
             return;
         }
 #pragma unroll
         for (int sl = 0; sl < BS / 16; ++sl) {
             const int nv = nvalid - 16 * sl;
             if (nv <= 0) break;
-            slice(Kt + sl * 16 * S::ROW, Vt + sl * 16 * S::ROW, nv, scale_log2);
+            slice(Kt + sl * 16 * S::ROW, Vt + sl * 16 * S::ROW, Ks + 16 * sl, Vs + 16 * sl, nv, scale_log2);
         }
     }
 
     __device__ __forceinline__ void block2(const unsigned char* Ka, const unsigned char* Va, int nva,
                                            const unsigned char* Kb, const unsigned char* Vb, int nvb,
                                            float scale_log2) {
-        slice2(Ka, Va, nva, Kb, Vb, nvb, scale_log2);
+        slice2(Ka, Va, nva, Kb, Vb, nvb, Ka + S::SCALES, Va + S::SCALES, Kb + S::SCALES, Vb + S::SCALES, scale_log2);
     }
 
     __device__ __forceinline__ void finish(const StageMeta& mt, const DecodeParams& p) {
@@ -800,13 +857,13 @@ template <typename TQ, typename TC, int G>
 struct UseMma {
     static constexpr bool value =
         sizeof(TQ) == 2 && ((std::is_same<TQ, TC>::value && (G == 4 || G == 8)) ||
-                            (std::is_same<TC, fp8e4m3>::value && G <= 8));
+                            (kIsFp8<TC> && G <= 8));
 };
 
 template <typename TQ, typename TC, int D, int BS, int G>
 using ConsumerFor = typename std::conditional<
     UseMma<TQ, TC, G>::value,
-    typename std::conditional<std::is_same<TC, fp8e4m3>::value, MmaConsumerFp8<TQ, D, BS, G>,
+    typename std::conditional<kIsFp8<TC>, MmaConsumerFp8<TQ, TC, D, BS, G>,
                               MmaConsumer<TQ, D, BS, G>>::type,
     FmaConsumer<TQ, TC, D, BS, G>>::type;
 
@@ -861,7 +918,7 @@ __device__ __forceinline__ int choose_partition(const int* s_len, int nseq, cons
 // cache, whose tiles are half the size) per CTA; the host picks the count.
 template <typename TQ, typename TC, int G>
 constexpr int decode_max_threads() {
-    return (std::is_same<TC, fp8e4m3>::value && UseMma<TQ, TC, G>::value) ? PKV_FP8_THREADS : 384;
+    return (kIsFp8<TC> && UseMma<TQ, TC, G>::value) ? PKV_FP8_THREADS : 384;
 }
 
 template <typename TQ, typename TC, int D, int BS, int G>
@@ -931,7 +988,7 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
     // Items of more than 32 blocks (partitions up to 64 blocks) only for
     // 16-bit caches and groups of 4+ heads; elsewhere the host keeps
     // partitions at 32 blocks or less and this code is left out.
-    constexpr bool kLongItems = !std::is_same<TC, fp8e4m3>::value && G >= 4;
+    constexpr bool kLongItems = !kIsFp8<TC> && G >= 4;
 
     auto fetch = [&](int idx) -> Item {
         Item it;
@@ -975,7 +1032,7 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
     int qslot_ctr = 0;    // q slot of P
     int issue_st = 0;
     int issued = 0;
-    const size_t tile_elems = (size_t)BS * D;
+    const size_t tile_elems = S::TILE / sizeof(TC);
     const TC* kc = reinterpret_cast<const TC*>(p.k_cache);
     const TC* vc = reinterpret_cast<const TC*>(p.v_cache);
     const TQ* qg = reinterpret_cast<const TQ*>(p.q);
@@ -1081,7 +1138,7 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
         // needs is held in registers and finish() reads the item's output rows
         // from the stage's metadata; the 16-bit kernels keep a copy (measured:
         // each way is the faster one for its kernel).
-        constexpr bool kLean = std::is_same<TC, fp8e4m3>::value;
+        constexpr bool kLean = kIsFp8<TC>;
         StageMeta mt;
         if constexpr (kLean) {
             mt.flags = meta[cons_st].flags;

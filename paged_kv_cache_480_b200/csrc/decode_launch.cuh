@@ -103,6 +103,9 @@ PKV_DECLARE_TYPES(bf16)
 PKV_DECLARE_TYPES(f32_fp8)
 PKV_DECLARE_TYPES(f16_fp8)
 PKV_DECLARE_TYPES(bf16_fp8)
+PKV_DECLARE_TYPES(f32_fp8row)
+PKV_DECLARE_TYPES(f16_fp8row)
+PKV_DECLARE_TYPES(bf16_fp8row)
 PKV_DECLARE_MERGE(f32)
 PKV_DECLARE_MERGE(f16)
 PKV_DECLARE_MERGE(bf16)

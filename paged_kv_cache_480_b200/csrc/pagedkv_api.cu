@@ -9,6 +9,7 @@
 #include "decode_tc.cuh"
 #include "pagedkv.h"
 #include "prefill.cuh"
+#include "row_ops.cuh"
 
 #ifndef PKV_FP8_WCAP
 #define PKV_FP8_WCAP 16
@@ -131,8 +132,15 @@ WorkspaceLayout workspace_layout(int num_seqs, int num_heads, int num_kv_heads, 
     return w;
 }
 
-uint32_t warp_smem(pkv_dtype t, bool fp8_cache, int D, int BS, int G, int R) {
-    if (fp8_cache) {
+uint32_t warp_smem(pkv_dtype t, pkv::CacheKind kind, int D, int BS, int G, int R) {
+    if (kind == pkv::CacheKind::kFp8Row) {
+        switch (t) {
+            case PKV_F32: return pkv::warp_smem_f32_fp8row(D, BS, G, R);
+            case PKV_F16: return pkv::warp_smem_f16_fp8row(D, BS, G, R);
+            default: return pkv::warp_smem_bf16_fp8row(D, BS, G, R);
+        }
+    }
+    if (kind == pkv::CacheKind::kFp8) {
         switch (t) {
             case PKV_F32: return pkv::warp_smem_f32_fp8(D, BS, G, R);
             case PKV_F16: return pkv::warp_smem_f16_fp8(D, BS, G, R);
@@ -215,7 +223,8 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
                        int head_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
                        pkv_dtype dtype, int partition_size, void* workspace,
                        size_t workspace_bytes, void* stream, const AppendArgs* app,
-                       bool fp8_cache = false, float k_scale = 1.f, float v_scale = 1.f) {
+                       pkv::CacheKind kind = pkv::CacheKind::kSame, float k_scale = 1.f, float v_scale = 1.f) {
+    const bool fp8_cache = kind != pkv::CacheKind::kSame;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens)
         return PKV_ERR_INVALID_ARG;
     pkv_status st = check_shape(num_seqs, num_heads, num_kv_heads, head_size, block_size,
@@ -290,10 +299,10 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     const bool fp8_mma = fp8_cache && dtype != PKV_F32;
     const int want = fp8_mma ? PKV_FP8_WCAP : (fp8_cache ? 12 : 8);
     int R = fp8_mma ? PKV_FP8_RMAX : 4;
-    uint32_t per_warp = warp_smem(dtype, fp8_cache, head_size, block_size, G, R);
+    uint32_t per_warp = warp_smem(dtype, kind, head_size, block_size, G, R);
     while (R > 2 && (pkv::kMaxDynSmem - seq_smem) / per_warp < (uint32_t)want) {
         --R;
-        per_warp = warp_smem(dtype, fp8_cache, head_size, block_size, G, R);
+        per_warp = warp_smem(dtype, kind, head_size, block_size, G, R);
     }
     int W = (int)((pkv::kMaxDynSmem - seq_smem) / per_warp);
     if (W > want) W = want;
@@ -346,7 +355,13 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     const dim3 grid(ctas), block(32 * W);
-    if (fp8_cache) {
+    if (kind == pkv::CacheKind::kFp8Row) {
+        switch (dtype) {
+            case PKV_F32: e = pkv::decode_f32_fp8row(p, head_size, block_size, G, grid, block, smem, s); break;
+            case PKV_F16: e = pkv::decode_f16_fp8row(p, head_size, block_size, G, grid, block, smem, s); break;
+            default: e = pkv::decode_bf16_fp8row(p, head_size, block_size, G, grid, block, smem, s); break;
+        }
+    } else if (fp8_cache) {
         switch (dtype) {
             case PKV_F32: e = pkv::decode_f32_fp8(p, head_size, block_size, G, grid, block, smem, s); break;
             case PKV_F16: e = pkv::decode_f16_fp8(p, head_size, block_size, G, grid, block, smem, s); break;
@@ -408,7 +423,17 @@ pkv_status paged_attention_decode_fp8kv(void* out, const void* q, const void* k_
     return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
                        block_size, num_seqs, num_heads, head_size, num_blocks, max_blocks_per_seq,
                        max_context_len, dtype, partition_size, workspace, workspace_bytes, stream,
-                       nullptr, true, k_scale, v_scale);
+                       nullptr, pkv::CacheKind::kFp8, k_scale, v_scale);
+}
+
+pkv_status paged_attention_decode_fp8row(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                         int num_kv_heads, int block_size, int num_seqs, int num_heads, int head_size,
+                                         int num_blocks, int max_blocks_per_seq, int max_context_len, pkv_dtype dtype,
+                                         int partition_size, void* workspace, size_t workspace_bytes, void* stream) {
+    return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, block_size, num_seqs,
+                       num_heads, head_size, num_blocks, max_blocks_per_seq, max_context_len, dtype, partition_size,
+                       workspace, workspace_bytes, stream, nullptr, pkv::CacheKind::kFp8Row);
 }
 
 pkv_status paged_attention_decode_append(void* out, const void* q, const void* key,
@@ -605,13 +630,16 @@ pkv_status swap_blocks(const void* const* src_caches, void* const* dst_caches, i
     return PKV_OK;
 }
 
-pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache,
-                                   const void* v_cache, const int32_t* block_tables,
-                                   const int32_t* context_lens, const int32_t* query_start_loc,
-                                   float scale, int num_tokens, int num_seqs, int num_heads,
-                                   int num_kv_heads, int head_size, int block_size,
-                                   int num_blocks, int max_blocks_per_seq, int max_query_len,
-                                   pkv_dtype dtype, void* stream) {
+}  // extern "C"
+
+namespace {
+
+pkv_status prefill_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, const int32_t* context_lens,
+                        const int32_t* query_start_loc, float scale, int num_tokens, int num_seqs, int num_heads,
+                        int num_kv_heads, int head_size, int block_size, int num_blocks, int max_blocks_per_seq,
+                        int max_query_len, pkv_dtype dtype, pkv::CacheKind kind, float k_scale, float v_scale,
+                        void* stream) {
     if (num_tokens < 0 || num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
         max_blocks_per_seq <= 0 || max_query_len < 0 || max_query_len > num_tokens)
         return PKV_ERR_INVALID_ARG;
@@ -623,6 +651,9 @@ pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache
     if ((int64_t)num_blocks * num_kv_heads * block_size >= (int64_t)0x7fffffff - block_size)
         return PKV_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || !(scale < INFINITY)) return PKV_ERR_INVALID_ARG;
+    if (!(k_scale > 0.f) || !(v_scale > 0.f)) return PKV_ERR_INVALID_ARG;
+    // (the softmax takes row maxima before the scale, so it has to stay positive)
+    if (!(scale * k_scale > 0.f) || !(scale * k_scale < INFINITY)) return PKV_ERR_INVALID_ARG;
     if (num_tokens == 0) return PKV_OK;
     if (max_query_len == 0) return PKV_ERR_INVALID_ARG;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc)
@@ -655,8 +686,266 @@ pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.max_query_len = max_query_len;
     a.dtype = dtype;
+    a.kind = kind;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
     a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     return pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables,
+                                   const int32_t* context_lens, const int32_t* query_start_loc,
+                                   float scale, int num_tokens, int num_seqs, int num_heads,
+                                   int num_kv_heads, int head_size, int block_size,
+                                   int num_blocks, int max_blocks_per_seq, int max_query_len,
+                                   pkv_dtype dtype, void* stream) {
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, num_tokens,
+                        num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks, max_blocks_per_seq,
+                        max_query_len, dtype, pkv::CacheKind::kSame, 1.f, 1.f, stream);
+}
+
+pkv_status paged_attention_prefill_fp8kv(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* context_lens,
+                                         const int32_t* query_start_loc, float scale, float k_scale, float v_scale,
+                                         int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                         int block_size, int num_blocks, int max_blocks_per_seq, int max_query_len,
+                                         pkv_dtype dtype, void* stream) {
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, num_tokens,
+                        num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks, max_blocks_per_seq,
+                        max_query_len, dtype, pkv::CacheKind::kFp8, k_scale, v_scale, stream);
+}
+
+pkv_status paged_attention_prefill_fp8row(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* query_start_loc, float scale, int num_tokens, int num_seqs,
+                                          int num_heads, int num_kv_heads, int head_size, int block_size,
+                                          int num_blocks, int max_blocks_per_seq, int max_query_len, pkv_dtype dtype,
+                                          void* stream) {
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, num_tokens,
+                        num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks, max_blocks_per_seq,
+                        max_query_len, dtype, pkv::CacheKind::kFp8Row, 1.f, 1.f, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Token strides in elements: at least a token's rows, a multiple of 16 bytes.
+bool good_stride(int64_t stride, int64_t row_elems, int elem) { return stride >= row_elems && (stride * elem) % 16 == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+int block_shift(int block_size) { return block_size == 32 ? 5 : 4; }
+
+// Checks and launch shared by the rotary calls and the quantising write
+// (rotary_dim 0, no q).  Sizes first, as in the other calls: with no tokens
+// the pointers are not looked at.
+pkv_status rotary_impl(pkv::RotaryParams& p, pkv::RowSink sink, int interleaved, int block_size, int num_blocks,
+                       pkv_dtype dtype, void* stream) {
+    const bool cache = sink != pkv::RowSink::kRows, rotated = p.rot > 0;
+    if (p.num_tokens < 0 || p.num_heads < 0 || p.num_kv_heads < 0 || p.rot < 0) return PKV_ERR_INVALID_ARG;
+    if (cache && (p.num_kv_heads == 0 || num_blocks <= 0)) return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (cache) {
+        if (p.head_size != 64 && p.head_size != 128) return PKV_ERR_UNSUPPORTED;
+        if (block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
+    } else if (p.head_size < 16 || p.head_size > 512 || p.head_size % 16 != 0) {
+        return PKV_ERR_UNSUPPORTED;
+    }
+    if (p.rot % 2 != 0 || p.rot > p.head_size) return PKV_ERR_INVALID_ARG;
+    if (!(std::fabs(p.mscale) < INFINITY)) return PKV_ERR_INVALID_ARG;
+    // one token's rows times the row's threads stay far inside 32 bits
+    if (p.num_heads > 65536 || p.num_kv_heads > 65536) return PKV_ERR_UNSUPPORTED;
+    if (p.num_tokens == 0 || p.num_heads + p.num_kv_heads == 0) return PKV_OK;
+    const int eb = elem_bytes(dtype);
+    const int64_t qrow = (int64_t)p.num_heads * p.head_size, krow = (int64_t)p.num_kv_heads * p.head_size;
+    if (rotated && (!p.positions || !p.inv_freq || !aligned8(p.positions) || !aligned4(p.inv_freq)))
+        return PKV_ERR_INVALID_ARG;
+    if (qrow > 0 && (!p.q || !p.q_out || !aligned16(p.q) || !aligned16(p.q_out) || !good_stride(p.q_stride, qrow, eb) ||
+                     !good_stride(p.q_out_stride, qrow, eb)))
+        return PKV_ERR_INVALID_ARG;
+    if (krow > 0 && (!p.k || !aligned16(p.k) || !good_stride(p.k_stride, krow, eb))) return PKV_ERR_INVALID_ARG;
+    if (cache) {
+        if (!p.v || !p.k_cache || !p.v_cache || !p.slot_mapping || !aligned16(p.v) || !aligned16(p.k_cache) ||
+            !aligned16(p.v_cache) || !aligned8(p.slot_mapping) || !good_stride(p.v_stride, krow, eb))
+            return PKV_ERR_INVALID_ARG;
+        p.block_shift = block_shift(block_size);
+        p.pool_slots = (int64_t)num_blocks * block_size;
+    } else if (krow > 0 && (!p.k_out || !aligned16(p.k_out) || !good_stride(p.k_out_stride, krow, eb))) {
+        return PKV_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    pkv_status st = device_info(&sms, &p.errors);
+    if (st != PKV_OK) return st;
+    return pkv::launch_rotary(p, sink, interleaved != 0, dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+pkv_status rotary_cache_impl(pkv::RowSink sink, void* q_out, const void* q, const void* key, const void* value,
+                             void* k_cache, void* v_cache, const int64_t* positions, const int64_t* slot_mapping,
+                             const float* inv_freq, int num_tokens, int num_heads, int num_kv_heads, int head_size,
+                             int rotary_dim, int interleaved, float attention_scale, int block_size, int num_blocks,
+                             int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             pkv_dtype dtype, void* stream) {
+    pkv::RotaryParams p{};
+    p.q = q;
+    p.k = key;
+    p.v = value;
+    p.q_out = q_out;
+    p.k_cache = static_cast<unsigned char*>(k_cache);
+    p.v_cache = static_cast<unsigned char*>(v_cache);
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.inv_freq = inv_freq;
+    p.q_out_stride = q_out_stride;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.mscale = attention_scale;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_size = head_size;
+    p.rot = rotary_dim;
+    return rotary_impl(p, sink, interleaved, block_size, num_blocks, dtype, stream);
+}
+
+pkv_status gather_impl(pkv::CacheKind kind, void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, const int32_t* start_loc, int num_tokens, int num_seqs,
+                       int num_kv_heads, int head_size, int block_size, int num_blocks, int max_blocks_per_seq,
+                       pkv_dtype dtype, float k_scale, float v_scale, void* stream) {
+    if (num_tokens < 0 || num_seqs <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_F32 && dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (head_size != 64 && head_size != 128) return PKV_ERR_UNSUPPORTED;
+    if (block_size != 16 && block_size != 32) return PKV_ERR_UNSUPPORTED;
+    if (num_kv_heads > 65536) return PKV_ERR_UNSUPPORTED;
+    if (!(k_scale > 0.f) || !(v_scale > 0.f)) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k_out || !v_out || !k_cache || !v_cache || !block_tables || !start_loc || !aligned16(k_out) ||
+        !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_tables) ||
+        !aligned4(start_loc))
+        return PKV_ERR_INVALID_ARG;
+    pkv::GatherParams p{};
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.k_cache = static_cast<const unsigned char*>(k_cache);
+    p.v_cache = static_cast<const unsigned char*>(v_cache);
+    p.block_tables = block_tables;
+    p.start_loc = start_loc;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.num_tokens = num_tokens;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.head_size = head_size;
+    p.block_shift = block_shift(block_size);
+    p.num_blocks = num_blocks;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    int sms = 0;
+    pkv_status st = device_info(&sms, &p.errors);
+    if (st != PKV_OK) return st;
+    return pkv::launch_gather(p, kind, dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                                    : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status rotary_embedding(void* q_out, void* k_out, const void* q, const void* k, const int64_t* positions,
+                            const float* inv_freq, int num_tokens, int num_heads, int num_kv_heads, int head_size,
+                            int rotary_dim, int interleaved, float attention_scale, int64_t q_out_token_stride,
+                            int64_t k_out_token_stride, int64_t q_token_stride, int64_t k_token_stride,
+                            pkv_dtype dtype, void* stream) {
+    if (rotary_dim <= 0) return PKV_ERR_INVALID_ARG;
+    pkv::RotaryParams p{};
+    p.q = q;
+    p.k = k;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.q_out_stride = q_out_token_stride;
+    p.k_out_stride = k_out_token_stride;
+    p.q_stride = q_token_stride;
+    p.k_stride = k_token_stride;
+    p.mscale = attention_scale;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_size = head_size;
+    p.rot = rotary_dim;
+    return rotary_impl(p, pkv::RowSink::kRows, interleaved, 16, 1, dtype, stream);
+}
+
+pkv_status rotary_reshape_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                                    void* v_cache, const int64_t* positions, const int64_t* slot_mapping,
+                                    const float* inv_freq, int num_tokens, int num_heads, int num_kv_heads,
+                                    int head_size, int rotary_dim, int interleaved, float attention_scale,
+                                    int block_size, int num_blocks, int64_t q_out_token_stride,
+                                    int64_t q_token_stride, int64_t key_token_stride, int64_t value_token_stride,
+                                    pkv_dtype dtype, void* stream) {
+    if (rotary_dim <= 0) return PKV_ERR_INVALID_ARG;
+    return rotary_cache_impl(pkv::RowSink::kCache, q_out, q, key, value, k_cache, v_cache, positions, slot_mapping,
+                             inv_freq, num_tokens, num_heads, num_kv_heads, head_size, rotary_dim, interleaved,
+                             attention_scale, block_size, num_blocks, q_out_token_stride, q_token_stride,
+                             key_token_stride, value_token_stride, dtype, stream);
+}
+
+pkv_status rotary_reshape_and_cache_fp8row(void* q_out, const void* q, const void* key, const void* value,
+                                           void* k_cache, void* v_cache, const int64_t* positions,
+                                           const int64_t* slot_mapping, const float* inv_freq, int num_tokens,
+                                           int num_heads, int num_kv_heads, int head_size, int rotary_dim,
+                                           int interleaved, float attention_scale, int block_size, int num_blocks,
+                                           int64_t q_out_token_stride, int64_t q_token_stride,
+                                           int64_t key_token_stride, int64_t value_token_stride, pkv_dtype dtype,
+                                           void* stream) {
+    if (rotary_dim <= 0) return PKV_ERR_INVALID_ARG;
+    return rotary_cache_impl(pkv::RowSink::kCacheFp8Row, q_out, q, key, value, k_cache, v_cache, positions,
+                             slot_mapping, inv_freq, num_tokens, num_heads, num_kv_heads, head_size, rotary_dim,
+                             interleaved, attention_scale, block_size, num_blocks, q_out_token_stride, q_token_stride,
+                             key_token_stride, value_token_stride, dtype, stream);
+}
+
+pkv_status reshape_and_cache_fp8row(const void* key, const void* value, void* k_cache, void* v_cache,
+                                    const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_size,
+                                    int block_size, int num_blocks, int64_t key_token_stride,
+                                    int64_t value_token_stride, pkv_dtype dtype, void* stream) {
+    return rotary_cache_impl(pkv::RowSink::kCacheFp8Row, nullptr, nullptr, key, value, k_cache, v_cache, nullptr,
+                             slot_mapping, nullptr, num_tokens, 0, num_kv_heads, head_size, 0, 1, 1.f, block_size,
+                             num_blocks, 0, 0, key_token_stride, value_token_stride, dtype, stream);
+}
+
+pkv_status gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, const int32_t* start_loc, int num_tokens, int num_seqs,
+                        int num_kv_heads, int head_size, int block_size, int num_blocks, int max_blocks_per_seq,
+                        pkv_dtype dtype, void* stream) {
+    return gather_impl(pkv::CacheKind::kSame, k_out, v_out, k_cache, v_cache, block_tables, start_loc, num_tokens,
+                       num_seqs, num_kv_heads, head_size, block_size, num_blocks, max_blocks_per_seq, dtype, 1.f, 1.f,
+                       stream);
+}
+
+pkv_status gather_cache_fp8kv(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* start_loc, float k_scale, float v_scale,
+                              int num_tokens, int num_seqs, int num_kv_heads, int head_size, int block_size,
+                              int num_blocks, int max_blocks_per_seq, pkv_dtype dtype, void* stream) {
+    return gather_impl(pkv::CacheKind::kFp8, k_out, v_out, k_cache, v_cache, block_tables, start_loc, num_tokens,
+                       num_seqs, num_kv_heads, head_size, block_size, num_blocks, max_blocks_per_seq, dtype, k_scale,
+                       v_scale, stream);
+}
+
+pkv_status gather_cache_fp8row(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, const int32_t* start_loc, int num_tokens, int num_seqs,
+                               int num_kv_heads, int head_size, int block_size, int num_blocks,
+                               int max_blocks_per_seq, pkv_dtype dtype, void* stream) {
+    return gather_impl(pkv::CacheKind::kFp8Row, k_out, v_out, k_cache, v_cache, block_tables, start_loc, num_tokens,
+                       num_seqs, num_kv_heads, head_size, block_size, num_blocks, max_blocks_per_seq, dtype, 1.f, 1.f,
+                       stream);
 }
 
 pkv_status pkv_set_wait_limit(int64_t polls) {

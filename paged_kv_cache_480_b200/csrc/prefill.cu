@@ -37,7 +37,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ba
     return encode_tiled(map, type, rank, base, dims, strides_bytes, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename T, int D, int BS>
+template <typename T, typename TC, int D, int BS>
 pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
     using S = PrefillShape<T, D, BS>;
     const int G = a.num_heads / a.num_kv_heads;
@@ -46,6 +46,7 @@ pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
     const CUtensorMapDataType type =
         std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t esz = sizeof(T);
+    constexpr bool kConvert = !std::is_same<T, TC>::value;
     alignas(64) CUtensorMap tm_q, tm_k, tm_v;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.num_heads, (cuuint64_t)a.num_tokens};
@@ -55,7 +56,9 @@ pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
     }
     const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * BS;
     if (rows > 0x7fffffff - BS) return PKV_ERR_UNSUPPORTED;
-    {
+    if constexpr (kConvert) {
+        tm_k = tm_v = tm_q;                  // not read
+    } else {
         const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
         const cuuint64_t strides[1] = {D * esz};
         const cuuint32_t box[2] = {64, (cuuint32_t)BS};
@@ -81,6 +84,10 @@ pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
     p.wait_limit = a.wait_limit;
     p.q_tiles = (a.max_query_len + 2 * QT - 1) / (2 * QT);
     p.cache_rows = (int)rows;
+    p.k_cache = static_cast<const unsigned char*>(a.k_cache);
+    p.v_cache = static_cast<const unsigned char*>(a.v_cache);
+    p.out_scale = a.v_scale;
+    if constexpr (kConvert) p.scale_log2 *= a.k_scale;
     int dev = 0, sms = 0, l2 = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PKV_ERR_CUDA;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -95,14 +102,14 @@ pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
     // mixed lengths); small ones keep a pair's items close in time, so its
     // K/V comes from DRAM about once (chunks of long contexts).
     {
-        const double pair_bytes = (double)a.max_blocks_per_seq * BS * D * sizeof(T) * 2.0;
+        const double pair_bytes = (double)a.max_blocks_per_seq * cache_tile_bytes<TC>(D, BS) * 2.0;
         const double in_flight = 0.75 * l2 / (pair_bytes > 1.0 ? pair_bytes : 1.0);
         const double g = in_flight - 1.5 * sms / (p.q_tiles > 0 ? p.q_tiles : 1);
         p.sched_group = g < 2.0 ? 2 : (g > 4096.0 ? 4096 : (int)g);
     }
     const int64_t items = (int64_t)p.q_tiles * a.num_seqs * a.num_kv_heads;
     if (items > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
-    auto kernel = paged_prefill_kernel<T, D, BS>;
+    auto kernel = paged_prefill_kernel<T, TC, D, BS>;
     static std::atomic<bool> configured[kMaxDevices];
     // persistent: one CTA per SM (fewer if there are fewer items)
     const int64_t grid = items < sms ? items : sms;
@@ -114,27 +121,36 @@ pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
             return PKV_ERR_CUDA;
         configured[dev].store(true, std::memory_order_release);
     }
-    if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kPrefillThreads), S::SMEM, stream, p, tm_q, tm_k,
+    if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kPrefillThreads<T, TC>), S::SMEM, stream, p, tm_q, tm_k,
                    tm_v) != cudaSuccess)
         return PKV_ERR_CUDA;
     return PKV_OK;
 }
 
-template <typename T, int D>
+template <typename T, typename TC, int D>
 pkv_status by_block(const PrefillArgs& a, cudaStream_t stream) {
     switch (a.block_size) {
-        case 16: return run<T, D, 16>(a, stream);
-        case 32: return run<T, D, 32>(a, stream);
+        case 16: return run<T, TC, D, 16>(a, stream);
+        case 32: return run<T, TC, D, 32>(a, stream);
+        default: return PKV_ERR_UNSUPPORTED;
+    }
+}
+
+template <typename T, typename TC>
+pkv_status by_head(const PrefillArgs& a, cudaStream_t stream) {
+    switch (a.head_size) {
+        case 64: return by_block<T, TC, 64>(a, stream);
+        case 128: return by_block<T, TC, 128>(a, stream);
         default: return PKV_ERR_UNSUPPORTED;
     }
 }
 
 template <typename T>
-pkv_status by_head(const PrefillArgs& a, cudaStream_t stream) {
-    switch (a.head_size) {
-        case 64: return by_block<T, 64>(a, stream);
-        case 128: return by_block<T, 128>(a, stream);
-        default: return PKV_ERR_UNSUPPORTED;
+pkv_status by_kind(const PrefillArgs& a, cudaStream_t stream) {
+    switch (a.kind) {
+        case CacheKind::kSame: return by_head<T, T>(a, stream);
+        case CacheKind::kFp8: return by_head<T, fp8e4m3>(a, stream);
+        default: return by_head<T, fp8row>(a, stream);
     }
 }
 
@@ -142,8 +158,8 @@ pkv_status by_head(const PrefillArgs& a, cudaStream_t stream) {
 
 pkv_status launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     switch (a.dtype) {
-        case PKV_F16: return by_head<__half>(a, stream);
-        case PKV_BF16: return by_head<__nv_bfloat16>(a, stream);
+        case PKV_F16: return by_kind<__half>(a, stream);
+        case PKV_BF16: return by_kind<__nv_bfloat16>(a, stream);
         default: return PKV_ERR_UNSUPPORTED;
     }
 }

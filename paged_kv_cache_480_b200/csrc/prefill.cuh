@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "pagedkv.h"
+#include "row_ops.cuh"
 
 namespace pkv {
 
@@ -21,6 +22,8 @@ struct PrefillArgs {
     int num_tokens, num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks;
     int max_blocks_per_seq, max_query_len;
     pkv_dtype dtype;
+    CacheKind kind;            // element kind of the caches
+    float k_scale, v_scale;    // kFp8: scales of all of K and of V; 1 otherwise
     uint32_t wait_limit;   // polls before a bounded wait gives up
 };
 

@@ -30,6 +30,8 @@
 //                      a context's end in its last block;
 //   warp 11            takes items from the counter, hands them to the other
 //                      roles through a ring in shared memory, and loads q.
+//   warps 12-15        E4M3 caches only, in place of warps 9 and 10: load the
+//                      codes of both streams and convert them (prefill_convert.cuh).
 // Per key tile i of N = 128 keys and query tile x, in tensor memory
 // columns [256x, 256x + 256): S_x (128 fp32 columns), P_x over the first 64
 // of them (16-bit pairs), O_x (D fp32 columns) after S_x:
@@ -55,6 +57,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "prefill_convert.cuh"
 #include "tc05.cuh"
 #include "tc_softmax.cuh"
 
@@ -75,6 +78,9 @@ struct PrefillParams {
     int q_tiles;                      // items (query-tile pairs) per (sequence, KV head)
     int sched_group;                  // (sequence, KV head) pairs per scheduling group, >= 1
     int cache_rows;                   // rows of the [NB * Hkv * bs][D] view of a cache
+    const unsigned char* k_cache;     // E4M3 caches only (the others go through tensor maps)
+    const unsigned char* v_cache;
+    float out_scale;                  // E4M3 caches only: scale of all of V
 };
 
 #ifndef PKV_PREFILL_KST128
@@ -116,7 +122,10 @@ struct PrefillShape {
     static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM");
 };
 
-constexpr uint32_t kPrefillThreads = 384;
+// An E4M3 cache takes a fourth warpgroup, whose warps convert the tiles (and
+// leaves the TMA warps 9 and 10 without work).
+template <typename T, typename TC>
+constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 512;
 
 // One work item as the scheduler hands it to the other roles.
 struct PrefillItem {
@@ -129,8 +138,9 @@ struct PrefillItem {
 };
 static_assert(sizeof(PrefillItem) == 64, "item slot");
 
-template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kPrefillThreads, 1)
+// T: element type of q and out; TC: element type of the caches (T, fp8e4m3 or fp8row)
+template <typename T, typename TC, int D, int BS>
+__global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     paged_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     using S = PrefillShape<T, D, BS>;
@@ -138,6 +148,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     constexpr int KST = S::KST, VST = S::VST, IR = S::IR;
     constexpr int N = S::N;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kConvert = !std::is_same<T, TC>::value;
+    constexpr uint32_t kFullArrivals = kConvert ? 4 : 1;   // the converting warps, or the TMA thread
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_s = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
@@ -169,7 +181,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     const uint32_t bar_fin = bar + 8 * (B0 + 9);
     PrefillItem* items = reinterpret_cast<PrefillItem*>(smem + S::OFF_ITEMS);
     uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + S::OFF_HOLD);
-    constexpr int kItemReaders = 11;                // warps 0-7, and warps 8, 9, 10 once each
+    // warps 0-7, and warp 8 and the K/V producers (9 and 10, or 12-15) once each
+    constexpr int kItemReaders = kConvert ? 13 : 11;
     if (threadIdx.x == 0) {
         for (int k = 0; k < IR; ++k) {
             mbar_init(bar_ifull(k), 1);
@@ -180,11 +193,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             mbar_init(bar_qempty(x), 1);
         }
         for (int st = 0; st < KST; ++st) {
-            mbar_init(bar_kfull(st), 1);
+            mbar_init(bar_kfull(st), kFullArrivals);
             mbar_init(bar_kempty(st), 1);
         }
         for (int st = 0; st < VST; ++st) {
-            mbar_init(bar_vfull(st), 1);
+            mbar_init(bar_vfull(st), kFullArrivals);
             mbar_init(bar_vempty(st), 1);
         }
         for (int x = 0; x < 2; ++x) {
@@ -199,8 +212,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     if (threadIdx.x == 32) {
         tc05::prefetch_tmap(&tm_q);
-        tc05::prefetch_tmap(&tm_k);
-        tc05::prefetch_tmap(&tm_v);
+        if constexpr (!kConvert) {
+            tc05::prefetch_tmap(&tm_k);
+            tc05::prefetch_tmap(&tm_v);
+        }
     }
     if (warp == 0) {
         tc05::tmem_alloc(smem_addr(tm_holder), S::TM_COLS);
@@ -322,7 +337,55 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             for (int x = 0; x < 2; ++x)
                 if (qloads[x] > 0) mbar_wait_bounded(bar_qfull(x), (qloads[x] - 1) & 1, kWaitLimit);
         __syncwarp();
-    } else if (warp >= 9) {
+    } else if (kConvert && warp >= 9) {
+        // ===================== converting producers: warps 12-15, K and V =====================
+        if constexpr (kConvert) {
+            const int w = warp - 12;
+            int jt = 0;                              // key tiles converted so far
+            bool ok = true;
+            TileCodes<T, TC, D, BS> kt, vt;
+            for (int j = 0; ok && w >= 0; ++j) {
+                PrefillItem it;
+                if (!take_item(j, it)) { ok = false; break; }
+                if (it.s < 0) break;
+                const int s = it.s, g = it.g;
+                const int nT = max(it.nT0, it.nT1);
+                const int nblk = (it.L + BS - 1) / BS;
+                auto tile_blocks = [&](int t) -> int {
+                    int phys = -1;
+                    const int lb = t * S::BPT + lane;
+                    if (lane < S::BPT && lb < nblk) {
+                        phys = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
+                        if (phys >= p.num_blocks) phys = -1;
+                        if (phys < 0 && w == 0) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                    }
+                    return phys;
+                };
+                // K and V alternate; each stream's next tile is on its way from
+                // global memory while the other's is converted
+                int tbl = tile_blocks(0);
+                kt.load(p.k_cache, tbl, Hkv, g, it.L, w, lane);
+                for (int t = 0; t < nT; ++t, ++jt) {
+                    const int next = t + 1 < nT ? tile_blocks(t + 1) : -1;
+                    vt.load(p.v_cache, tbl, Hkv, g, it.L - t * N, w, lane);
+                    const int sk = jt % KST, sv = jt % VST;
+                    if (jt >= KST && !warp_wait(bar_kempty(sk), ((jt / KST) - 1) & 1, wl)) { ok = false; break; }
+                    kt.store(k_base(sk), w, lane);
+                    fence_proxy_async();             // before the tensor core reads the tile
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_kfull(sk));
+                    if (t + 1 < nT) kt.load(p.k_cache, next, Hkv, g, it.L - (t + 1) * N, w, lane);
+                    if (jt >= VST && !warp_wait(bar_vempty(sv), ((jt / VST) - 1) & 1, wl)) { ok = false; break; }
+                    vt.store(v_base(sv), w, lane);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_vfull(sv));
+                    tbl = next;
+                }
+            }
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+        }
+    } else if (!kConvert && warp >= 9) {
         // ===================== TMA producers: warp 9 K, warp 10 V =====================
         const bool is_v = warp == 10;
         const int nst = is_v ? VST : KST;
@@ -430,7 +493,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 if (it.s < 0) break;
                 const int nT0 = it.nT0, nT1 = it.nT1, nT = max(nT0, nT1);
                 const bool two = nT1 > 0;
-                const bool vz = it.vz_r0 < it.vz_r1;
+                const bool vz = !kConvert && it.vz_r0 < it.vz_r1;   // (converted tiles come with zeros there)
                 const int vz_x = nT0 == nT ? 0 : 1;            // the first product reading the last V tile
                 auto qk = [&](int x, int i) {                  // S_x = Q_x K_i^T
                     const uint32_t d = tm + x * S::TM_TILE + S::TM_S;
@@ -541,7 +604,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             // ---- O / l to the output ----
             if (ok && warp_wait(bar_o(x), ox & 1, wl)) {
                 tc05::fence_after_sync();
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l > 0.f ? (kConvert ? p.out_scale : 1.f) / l : 0.f;
                 T* orow = reinterpret_cast<T*>(p.out) +
                           ((size_t)(it.q0 + qi) * p.num_heads + (size_t)it.g * G + (r % G)) * D;
 #pragma unroll

@@ -1,0 +1,388 @@
+// Row kernels around the paged cache: rotary positions of q and k (alone, or
+// fused with the cache write), the quantising cache write, and the read-back
+// of whole sequences.  All are bound by HBM (each element is read and written
+// once) for many tokens and by latency for a few.
+#include "common.cuh"
+#include "fp8row.cuh"
+#include "pagedkv.h"
+#include "row_ops.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Row lengths are multiples of 2 * kPerChunk elements, and a thread takes
+// kPerChunk pairs of one row: rotary pairs (2i, 2i + 1) or (i, i + rot / 2),
+// and beyond the rotated part neighbours.  Both 16-byte chunks of a unit are
+// loaded and stored whole (VEC) unless the half layout's offset rot / 2 is
+// not a whole number of chunks, when the unit's elements go one by one.  A
+// pair lives in one thread, so q_out may be q and k_out may be k.
+template <typename T, bool INTERLEAVED, bool VEC>
+struct Unit {
+    static constexpr int E = Elem<T>::kPerChunk;
+
+    // first elements of the unit's two chunks (VEC)
+    __device__ __forceinline__ static int2 chunks(int u, int rot) {
+        const int i0 = u * E;
+        if (!INTERLEAVED && i0 < rot / 2) return make_int2(i0, i0 + rot / 2);
+        return make_int2(2 * i0, 2 * i0 + E);
+    }
+    // element index of pair i's first and second element
+    __device__ __forceinline__ static int2 pair(int i, int rot) {
+        if (!INTERLEAVED && i < rot / 2) return make_int2(i, i + rot / 2);
+        return make_int2(2 * i, 2 * i + 1);
+    }
+
+    // x[j], x[E + j]: the unit's j-th pair if `halves`, else x in memory order
+    __device__ __forceinline__ static void load(const T* row, int u, int rot, float (&x)[2 * E]) {
+        if constexpr (VEC) {
+            const int2 c = chunks(u, rot);
+            const uint4 a = *reinterpret_cast<const uint4*>(row + c.x);
+            const uint4 b = *reinterpret_cast<const uint4*>(row + c.y);
+            Elem<T>::widen(a, x);
+            Elem<T>::widen(b, x + E);
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int2 c = pair(u * E + j, rot);
+                x[j] = (float)row[c.x];
+                x[E + j] = (float)row[c.y];
+            }
+        }
+    }
+
+    __device__ __forceinline__ static void rotate(const float2* cs, int u, int rot, float (&x)[2 * E]) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int i = u * E + j;
+            float& a = x[INTERLEAVED ? 2 * j : j];
+            float& b = x[INTERLEAVED ? 2 * j + 1 : E + j];
+            if (i < rot / 2) {
+                const float2 w = cs[i];
+                const float y = a * w.x - b * w.y;
+                b = b * w.x + a * w.y;
+                a = y;
+            }
+        }
+    }
+
+    __device__ __forceinline__ static void store(T* row, int u, int rot, const float (&x)[2 * E]) {
+        if constexpr (VEC) {
+            const int2 c = chunks(u, rot);
+            *reinterpret_cast<uint4*>(row + c.x) = Elem<T>::narrow(x);
+            *reinterpret_cast<uint4*>(row + c.y) = Elem<T>::narrow(x + E);
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int2 c = pair(u * E + j, rot);
+                row[c.x] = (T)x[j];
+                row[c.y] = (T)x[E + j];
+            }
+        }
+    }
+
+    // E codes of one chunk as bytes, E = 4 or 8
+    __device__ __forceinline__ static void codes(const float* x, float mult, uint32_t (&w)[E / 4]) {
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) {
+            const uint32_t lo = f32x2_to_e4m3x2(x[4 * j] * mult, x[4 * j + 1] * mult);
+            const uint32_t hi = f32x2_to_e4m3x2(x[4 * j + 2] * mult, x[4 * j + 3] * mult);
+            w[j] = lo | (hi << 16);
+        }
+    }
+    __device__ __forceinline__ static void store_codes(unsigned char* row, int u, int rot, const float (&x)[2 * E],
+                                                       float mult) {
+        uint32_t a[E / 4], b[E / 4];
+        codes(x, mult, a);
+        codes(x + E, mult, b);
+        if constexpr (VEC) {
+            const int2 c = chunks(u, rot);
+            if constexpr (E == 8) {
+                *reinterpret_cast<uint2*>(row + c.x) = make_uint2(a[0], a[1]);
+                *reinterpret_cast<uint2*>(row + c.y) = make_uint2(b[0], b[1]);
+            } else {
+                *reinterpret_cast<uint32_t*>(row + c.x) = a[0];
+                *reinterpret_cast<uint32_t*>(row + c.y) = b[0];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int2 c = pair(u * E + j, rot);
+                row[c.x] = (unsigned char)(a[j / 4] >> (8 * (j % 4)));
+                row[c.y] = (unsigned char)(b[j / 4] >> (8 * (j % 4)));
+            }
+        }
+    }
+};
+
+// cos and sin of position * inv_freq.  The product and its reduction to a
+// fraction of a turn are in fp64 (an fp32 angle of a far position is off by
+// whole radians); the fraction, below half a turn, is exact enough in fp32.
+__device__ __forceinline__ float2 turn(int64_t position, float inv_freq, float mscale) {
+    const double t = (double)position * (double)inv_freq * 0.15915494309189535;   // 1 / (2 pi)
+    const float f = (float)(t - rint(t));
+    float s, c;
+    sincospif(2.f * f, &s, &c);
+    return make_float2(c * mscale, s * mscale);
+}
+
+// grid.x takes tokens (tokens_cta a CTA), grid.y parts of a token's units (a
+// few tokens are spread over the SMs that way).  The CTA first takes cos and
+// sin of its tokens' positions, one thread a frequency, into shared memory
+// where every head of the token reads them: with up to a hundred rows a token
+// the angles cost a few percent of the row work.
+template <typename T, RowSink SINK, bool INTERLEAVED, bool VEC>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+    using U = Unit<T, INTERLEAVED, VEC>;
+    using UV = Unit<T, true, true>;        // rows that are not rotated: plain chunks
+    constexpr int E = U::E;
+    extern __shared__ float2 cs_all[];
+    griddep_wait();
+    griddep_launch();
+    const int half = p.rot / 2;
+    const int64_t token0 = (int64_t)blockIdx.x * p.tokens_cta;
+    const int tokens = (int)min((int64_t)p.tokens_cta, p.num_tokens - token0);
+    for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+        const int t = i / half;
+        cs_all[i] = turn(p.positions[token0 + t], p.inv_freq[i - t * half], p.mscale);
+    }
+    __syncthreads();
+
+    const int first = blockIdx.y * p.units_cta;
+    const int last = min(first + p.units_cta, p.units_token * tokens);
+    const int D = p.head_size;
+    // whole warps stay in the loop: quantised rows shuffle over their lanes
+    for (int base = first + (threadIdx.x & ~31); base < last; base += blockDim.x) {
+        const int w = base + (threadIdx.x & 31);
+        const bool on = w < last;
+        const int t = on ? w / p.units_token : 0;
+        const int rem = on ? w - t * p.units_token : 0;
+        const int row = rem / p.units_row, u = rem - row * p.units_row;
+        const int64_t token = token0 + t;
+        const float2* cs = cs_all + t * half;
+        float x[2 * E];
+        if (row < p.num_heads) {
+            if (on) {
+                U::load(static_cast<const T*>(p.q) + token * p.q_stride + (int64_t)row * D, u, p.rot, x);
+                U::rotate(cs, u, p.rot, x);
+                U::store(static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)row * D, u, p.rot, x);
+            }
+            if constexpr (SINK != RowSink::kCacheFp8Row) continue;
+        }
+        if constexpr (SINK == RowSink::kRows) {
+            const int g = row - p.num_heads;
+            if (on) {
+                U::load(static_cast<const T*>(p.k) + token * p.k_stride + (int64_t)g * D, u, p.rot, x);
+                U::rotate(cs, u, p.rot, x);
+                U::store(static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)g * D, u, p.rot, x);
+            }
+        } else {
+            const bool kv = on && row >= p.num_heads;
+            const bool is_v = row >= p.num_heads + p.num_kv_heads;
+            const int g = row - p.num_heads - (is_v ? p.num_kv_heads : 0);
+            int64_t slot = -1;
+            if (kv) {
+                slot = p.slot_mapping[token];
+                if (slot >= p.pool_slots) {
+                    if (u == 0 && g == 0 && !is_v) flag_error(p.errors, PKV_DEVERR_SLOT);
+                    slot = -1;
+                }
+            }
+            const bool put = slot >= 0;
+            if (put) {
+                if (is_v) {
+                    UV::load(static_cast<const T*>(p.v) + token * p.v_stride + (int64_t)g * D, u, 0, x);
+                } else {
+                    U::load(static_cast<const T*>(p.k) + token * p.k_stride + (int64_t)g * D, u, p.rot, x);
+                    U::rotate(cs, u, p.rot, x);
+                }
+            }
+            const int64_t blk = slot >> p.block_shift;
+            const int bs = 1 << p.block_shift;
+            const int off = (int)(slot & (bs - 1));
+            unsigned char* cache = is_v ? p.v_cache : p.k_cache;
+            if constexpr (SINK == RowSink::kCache) {
+                if (put) {
+                    T* dst = reinterpret_cast<T*>(cache) + ((blk * p.num_kv_heads + g) * bs + off) * D;
+                    if (is_v) UV::store(dst, u, 0, x);
+                    else U::store(dst, u, p.rot, x);
+                }
+            } else {
+                // the row's largest magnitude over its D / (2 E) lanes
+                uint32_t top = 0;
+                if (put) {
+#pragma unroll
+                    for (int j = 0; j < 2 * E; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+                }
+                for (int o = 1; o < p.units_row; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (put) {
+                    const int b = row_scale_byte(top);
+                    unsigned char* tile = cache + (blk * p.num_kv_heads + g) * (int64_t)(bs * (D + 1));
+                    if (is_v) UV::store_codes(tile + off * D, u, 0, x, row_scale_inv(b));
+                    else U::store_codes(tile + off * D, u, p.rot, x, row_scale_inv(b));
+                    if (u == 0) tile[bs * D + off] = (unsigned char)b;
+                }
+            }
+        }
+    }
+}
+
+template <typename T, RowSink SINK>
+cudaError_t run_rotary(RotaryParams& p, bool interleaved, int num_sms, cudaStream_t stream) {
+    constexpr int E = Elem<T>::kPerChunk;
+    p.units_row = p.head_size / (2 * E);
+    const int rows = p.num_heads + p.num_kv_heads * (SINK == RowSink::kRows ? 1 : 2);
+    p.units_token = rows * p.units_row;
+    if (p.num_tokens == 0 || p.units_token == 0) return cudaSuccess;
+    // A CTA takes whole tokens, enough of them for two units a thread (at most
+    // 8 tokens: their angles stay within 16 KB); with too few such CTAs for the
+    // SMs a token's units are split into parts of one unit a thread.
+    const int want = 2 * kThreads;
+    int tpc = want / p.units_token;
+    tpc = tpc < 1 ? 1 : tpc > 8 ? 8 : tpc;
+    while (tpc > 1 && (p.num_tokens + tpc - 1) / tpc < 4 * num_sms) tpc >>= 1;
+    const int groups = (p.num_tokens + tpc - 1) / tpc;
+    p.tokens_cta = tpc;
+    p.units_cta = p.units_token * tpc;
+    int parts = 1;
+    if (tpc == 1 && groups < 4 * num_sms) {
+        const int most = (p.units_token + kThreads - 1) / kThreads;
+        parts = (4 * num_sms + groups - 1) / groups;
+        if (parts > most) parts = most;
+        p.units_cta = ((p.units_token + parts - 1) / parts + 31) / 32 * 32;
+        parts = (p.units_token + p.units_cta - 1) / p.units_cta;
+    }
+    int threads = (p.units_cta + 31) / 32 * 32;
+    if (threads > kThreads) threads = kThreads;
+    const size_t smem = sizeof(float2) * (size_t)tpc * (p.rot / 2);
+    const dim3 grid((unsigned)groups, (unsigned)parts), block((unsigned)threads);
+    if (interleaved) return launch_pdl(rotary_kernel<T, SINK, true, true>, grid, block, smem, stream, p);
+    if ((p.rot / 2) % E == 0) return launch_pdl(rotary_kernel<T, SINK, false, true>, grid, block, smem, stream, p);
+    return launch_pdl(rotary_kernel<T, SINK, false, false>, grid, block, smem, stream, p);
+}
+
+template <typename T>
+cudaError_t by_sink(RotaryParams& p, RowSink sink, bool interleaved, int num_sms, cudaStream_t stream) {
+    switch (sink) {
+        case RowSink::kRows: return run_rotary<T, RowSink::kRows>(p, interleaved, num_sms, stream);
+        case RowSink::kCache: return run_rotary<T, RowSink::kCache>(p, interleaved, num_sms, stream);
+        default: return run_rotary<T, RowSink::kCacheFp8Row>(p, interleaved, num_sms, stream);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Read-back: rows of the sequences' tokens from the pages to packed [N][Hkv][D].
+// A CTA takes a run of tokens; a thread finds each token's sequence (the last
+// one that starts at or before it) and block once, then the threads copy or
+// convert 16 cache bytes each, K and V.
+// ---------------------------------------------------------------------------
+constexpr int kGatherTokens = 32;
+
+template <typename T, CacheKind KIND>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
+    constexpr int ES = KIND == CacheKind::kSame ? (int)sizeof(T) : 1;   // bytes of a cache element
+    constexpr int EPU = 16 / ES;                                        // elements of a unit
+    __shared__ int s_phys[kGatherTokens];   // physical block; -1: zeros (a bad id); -2: no row
+    __shared__ int s_off[kGatherTokens];
+    griddep_wait();
+    griddep_launch();
+    const int64_t n0 = (int64_t)blockIdx.x * p.tokens_cta;
+    const int tokens = (int)min((int64_t)p.tokens_cta, p.num_tokens - n0);
+    if ((int)threadIdx.x < tokens) {
+        const int64_t n = n0 + threadIdx.x;
+        int lo = 0, hi = p.num_seqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.start_loc[mid] <= n) lo = mid; else hi = mid - 1;
+        }
+        const int64_t t = n - p.start_loc[lo];
+        int phys = -2, off = 0;
+        if (t >= 0 && n < p.start_loc[lo + 1]) {
+            const int64_t j = t >> p.block_shift;
+            if (j < p.max_blocks_per_seq) {
+                phys = p.block_tables[(int64_t)lo * p.max_blocks_per_seq + j];
+                off = (int)(t & ((1 << p.block_shift) - 1));
+                if (phys < 0 || phys >= p.num_blocks) {
+                    flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                    phys = -1;
+                }
+            } else {
+                flag_error(p.errors, PKV_DEVERR_CONTEXT);
+            }
+        }
+        s_phys[threadIdx.x] = phys;
+        s_off[threadIdx.x] = off;
+    }
+    __syncthreads();
+    const int D = p.head_size, bs = 1 << p.block_shift;
+    const int upr = D / EPU, per_token = 2 * p.num_kv_heads * upr;
+    const int64_t tile = KIND == CacheKind::kFp8Row ? (int64_t)bs * (D + 1) : (int64_t)bs * D * ES;
+    for (int w = threadIdx.x; w < tokens * per_token; w += blockDim.x) {
+        const int i = w / per_token;
+        int rem = w - i * per_token;
+        const bool is_v = rem >= per_token / 2;
+        if (is_v) rem -= per_token / 2;
+        const int g = rem / upr, u = rem - g * upr;
+        const int phys = s_phys[i];
+        if (phys == -2) continue;
+        T* dst = static_cast<T*>(is_v ? p.v_out : p.k_out) + ((n0 + i) * p.num_kv_heads + g) * D + u * EPU;
+        uint4 c = make_uint4(0u, 0u, 0u, 0u);
+        const unsigned char* base = (is_v ? p.v_cache : p.k_cache) + ((int64_t)phys * p.num_kv_heads + g) * tile;
+        if (phys >= 0) c = *reinterpret_cast<const uint4*>(base + (s_off[i] * D + u * EPU) * ES);
+        if constexpr (KIND == CacheKind::kSame) {
+            *reinterpret_cast<uint4*>(dst) = c;
+        } else {
+            float f[16], sc = is_v ? p.v_scale : p.k_scale;
+            if constexpr (KIND == CacheKind::kFp8Row) sc = phys >= 0 ? row_scale(base[bs * D + s_off[i]]) : 0.f;
+            Elem<fp8e4m3>::widen(c, f);
+            constexpr int E = Elem<T>::kPerChunk;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] *= sc;
+#pragma unroll
+            for (int j = 0; j < 16 / E; ++j) reinterpret_cast<uint4*>(dst)[j] = Elem<T>::narrow(f + j * E);
+        }
+    }
+}
+
+template <typename T, CacheKind KIND>
+cudaError_t run_gather(GatherParams& p, int num_sms, cudaStream_t stream) {
+    if (p.num_tokens == 0) return cudaSuccess;
+    // enough tokens for eight units a thread, fewer while the SMs are not filled
+    const int per_token = 2 * p.num_kv_heads * p.head_size / (KIND == CacheKind::kSame ? 16 / (int)sizeof(T) : 16);
+    int tpc = 8 * kThreads / per_token;
+    tpc = tpc < 1 ? 1 : tpc > kGatherTokens ? kGatherTokens : tpc;
+    while (tpc > 1 && (p.num_tokens + tpc - 1) / tpc < 4 * num_sms) tpc >>= 1;
+    p.tokens_cta = tpc;
+    const dim3 grid((unsigned)((p.num_tokens + tpc - 1) / tpc));
+    return launch_pdl(gather_kernel<T, KIND>, grid, dim3(kThreads), 0, stream, p);
+}
+
+template <typename T>
+cudaError_t by_kind(GatherParams& p, CacheKind kind, int num_sms, cudaStream_t stream) {
+    switch (kind) {
+        case CacheKind::kSame: return run_gather<T, CacheKind::kSame>(p, num_sms, stream);
+        case CacheKind::kFp8: return run_gather<T, CacheKind::kFp8>(p, num_sms, stream);
+        default: return run_gather<T, CacheKind::kFp8Row>(p, num_sms, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(RotaryParams p, RowSink sink, bool interleaved, int dtype, int num_sms, cudaStream_t stream) {
+    switch (dtype) {
+        case PKV_F32: return by_sink<float>(p, sink, interleaved, num_sms, stream);
+        case PKV_F16: return by_sink<__half>(p, sink, interleaved, num_sms, stream);
+        default: return by_sink<__nv_bfloat16>(p, sink, interleaved, num_sms, stream);
+    }
+}
+
+cudaError_t launch_gather(GatherParams p, CacheKind kind, int dtype, int num_sms, cudaStream_t stream) {
+    switch (dtype) {
+        case PKV_F32: return by_kind<float>(p, kind, num_sms, stream);
+        case PKV_F16: return by_kind<__half>(p, kind, num_sms, stream);
+        default: return by_kind<__nv_bfloat16>(p, kind, num_sms, stream);
+    }
+}
+
+}  // namespace pkv
