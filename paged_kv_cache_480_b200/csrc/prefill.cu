@@ -39,7 +39,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ba
 
 template <typename T, typename TC, int D, int BS>
 pkv_status run(const PrefillArgs& a, cudaStream_t stream) {
-    using S = PrefillShape<T, D, BS>;
+    using S = PrefillShape<T, TC, D, BS>;
     const int G = a.num_heads / a.num_kv_heads;
     if (G < 1 || G > kPrefillMaxGroup) return PKV_ERR_UNSUPPORTED;
     const int QT = S::M / G;                 // queries per query tile

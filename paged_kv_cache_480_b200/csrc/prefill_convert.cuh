@@ -4,9 +4,9 @@
 // 128-byte-swizzled layout that TMA gives the 16-bit caches.
 //
 // A code has four significant bits, so code * 2^e is exact in 16 bits but at
-// the ends of fp16's range.  Codes come straight from global memory into
-// registers, a whole tile ahead of their conversion (16 KB in flight a stream
-// and SM), so they need no staging in shared memory.
+// the ends of fp16's range.  The codes come through bulk copies, not loads
+// into registers: the proxy fence after each converted tile would wait for
+// outstanding loads, and with them for a memory latency a tile (measured).
 #pragma once
 
 #include <type_traits>
@@ -33,103 +33,161 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t twice16(uint32_t h) { return h | (h << 16); }
 
-// 16 codes of one row with scale byte b, as 16-bit values: lo holds codes 0-7.
+// 16 codes times the pair multiplier m, as 16-bit values: lo holds codes 0-7.
+// m is 2^e in both halves for fp16 (unused without row scales), 2^(120 + e) for
+// bf16.
 template <typename T, bool ROW>
-__device__ __forceinline__ void convert16(const uint4& c, int b, uint4& lo, uint4& hi) {
+__device__ __forceinline__ void convert16(const uint4& c, uint32_t m, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t o[8];
-    if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
             o[2 * i] = e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu));
             o[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(w[i] >> 16));
-        }
-        if constexpr (ROW) {
-            // 2^e as an fp16 multiplier: one rounding.  Outside fp16's powers
-            // of two, two steps of which the first is exact (down: codes are
-            // multiples of 2^-9, times 2^-12 still of 2^-21) or overflows (up).
-            const int e = b - 127;
-            uint32_t m = e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (max(e, -24) + 24);
-            if (e < -24 || e > 15) {
-                const uint32_t first = twice16(b == kRowScaleNan ? 0x7fffu : e < 0 ? 3u << 10 : 30u << 10);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], first);
-                const int r = e < 0 ? e + 12 : min(e - 15, 15);
-                m = r >= -14 ? (uint32_t)(r + 15) << 10 : 1u << (max(r, -24) + 24);
+            if constexpr (ROW) {
+                o[2 * i] = mul_f16x2(o[2 * i], m);
+                o[2 * i + 1] = mul_f16x2(o[2 * i + 1], m);
             }
-            m = twice16(m);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], m);
-        }
-    } else {
-        const int e = ROW ? b - 127 : 0;
-        // 2^(120 + e): one exact product; two where that is above bf16's largest
-        uint32_t m = 0x7b80u;
-        if constexpr (ROW) m = b == kRowScaleNan ? 0x7fffu : e <= 7 ? (uint32_t)(b + 120) << 7 : 0x7b80u;
-        m = twice16(m);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        } else {
             o[2 * i] = mul_bf16x2(e4m3_hi_to_bf16x2_raw(__byte_perm(w[i], 0, 0x1404)), m);
             o[2 * i + 1] = mul_bf16x2(e4m3_hi_to_bf16x2_raw(__byte_perm(w[i], 0, 0x3424)), m);
-        }
-        if (ROW && e > 7 && b != kRowScaleNan) {
-            const uint32_t up = twice16((uint32_t)b << 7);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], up);
         }
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// One thread's share of a 128-key tile: NJ pieces of 16 codes.  A warp step
-// covers 512 contiguous bytes of codes; within it the lanes are ordered so
-// that the eight lanes of a shared-memory phase write eight different 16-byte
-// columns of the swizzled rows (even columns from one row, odd from the next).
+// Pair multipliers of scale bytes: one multiply-add for the exponents whose
+// multiplier is a normal number of the type, fp16: -14 .. 15, bf16: up to 7
+// (down to the -60 of the format).  A slice with any other byte takes
+// scale_up, two products: the first exact (down: codes are multiples of 2^-9,
+// times 2^-12 still of 2^-21) or an overflow (up).
+template <typename T>
+struct PairScale {
+    static constexpr bool kHalf = std::is_same<T, __half>::value;
+    static constexpr int LO = kHalf ? 127 - 14 : 1, HI = kHalf ? 127 + 15 : 127 + 7;
+    __device__ __forceinline__ static uint32_t of(int b) {
+        return kHalf ? (uint32_t)(b - 112) * 0x04000400u : (uint32_t)(b + 120) * 0x00800080u;
+    }
+    // m for the byte, and a second multiplier
+    __device__ __forceinline__ static uint32_t first(int b) {
+        if (b == kRowScaleNan) return 0x7fff7fffu;
+        return kHalf ? of(b < LO ? 127 - 12 : HI) : of(127);
+    }
+    __device__ __forceinline__ static uint32_t second(int b) {
+        if (b == kRowScaleNan) return of(127);
+        if constexpr (kHalf) {
+            const int r = b < LO ? b + 12 : min(b - 15, HI);          // byte of the rest
+            return twice16(r >= LO ? (uint32_t)(r - 112) << 10 : 1u << (max(r, 127 - 24) - 103));
+        }
+        return twice16((uint32_t)b << 7);                             // 2^e as bf16
+    }
+};
+
+// One warp's 32 rows of a 128-key tile: bulk copies bring them from their
+// blocks into the warp's own staging slot (each block's rows, then its scale
+// bytes), the warp takes them into registers, requests its rows of the next
+// tile into the same slot, and converts.  A lane holds NJ pieces of 16 codes
+// of neighbouring rows.  Pieces are dealt so that the eight lanes of a
+// shared-memory phase touch eight different 16-byte columns, both reading the
+// slot (two rows of opposite halves, or of opposite parity for 64 dims) and
+// writing the swizzled tile (rows of opposite parity).
 template <typename T, typename TC, int D, int BS>
-struct TileCodes {
-    static constexpr int RPW = 512 / D;          // rows a warp step covers
-    static constexpr int RPS = 4 * RPW;          // rows the four warps cover
-    static constexpr int NJ = 128 / RPS;
-    static constexpr bool kRow = kRowScaled<TC>;
+struct SliceCodes {
+    static constexpr int ROWS = 32;
+    static constexpr int BLOCKS = ROWS / BS;            // blocks of a slice
     static constexpr int TILE = cache_tile_bytes<TC>(D, BS);
+    static constexpr int SLOT = BLOCKS * TILE;          // staging bytes
+    static constexpr int NJ = D / 16;                   // pieces (rows) a lane holds
+    static constexpr bool kRow = kRowScaled<TC>;
+    static_assert(D == 64 || D == 128, "head size");
+    static_assert(BLOCKS * BS == ROWS && BS % NJ == 0, "a lane's rows lie in one block");
 
     uint4 c[NJ];
-    int b[kRow ? NJ : 1];
+    uint32_t sb[NJ / 4];                                // their scale bytes, in the order of c
 
-    __device__ __forceinline__ static int dim0(int lane) { return (lane & 3) * 16 + (D == 128 ? ((lane >> 3) & 1) * 64 : 0); }
-    __device__ __forceinline__ static int row0(int w, int lane) {
-        return w * RPW + (D == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2);
+    __device__ __forceinline__ static int odd(int lane) { return (lane >> 2) & 1; }
+    // first of the lane's NJ rows; piece j is row first + (j ^ odd)
+    __device__ __forceinline__ static int first(int lane) {
+        return NJ * (D == 128 ? odd(lane) | ((lane >> 4) << 1) : lane >> 2);
+    }
+    __device__ __forceinline__ static int dim0(int lane) {
+        return (lane & 3) * 16 + (D == 128 ? 64 * (((lane >> 3) & 1) ^ odd(lane)) : 0);
     }
 
-    // tbl: lane j holds the tile's j-th physical block id (negative: none);
-    // rows past nrows of the tile and rows of no block read as zeros
-    __device__ __forceinline__ void load(const unsigned char* cache, int tbl, int Hkv, int g, int nrows, int w, int lane) {
+    __device__ __forceinline__ void load(uint32_t slot, int lane) {
+        const int r0 = first(lane);
+        const uint32_t base = slot + (r0 / BS) * TILE;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int t = j * RPS + row0(w, lane);
-            const int phys = __shfl_sync(0xffffffffu, tbl, t / BS);
-            c[j] = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (kRow) b[j] = 127;
-            if (t < nrows && phys >= 0) {
-                const unsigned char* tile = cache + ((int64_t)phys * Hkv + g) * TILE;
-                c[j] = __ldg(reinterpret_cast<const uint4*>(tile + (t % BS) * D + dim0(lane)));
-                if constexpr (kRow) b[j] = __ldg(tile + BS * D + t % BS);
+        for (int j = 0; j < NJ; ++j) c[j] = lds128(base + (r0 % BS + (j ^ odd(lane))) * D + dim0(lane));
+        if constexpr (kRow) {
+#pragma unroll
+            for (int k = 0; k < NJ / 4; ++k) {
+                sb[k] = (uint32_t)lds32(base + BS * D + r0 % BS + 4 * k);
+                if (odd(lane)) sb[k] = __byte_perm(sb[k], 0, 0x2301);
             }
         }
     }
 
-    // into the swizzled tile at shared address dst (64-dim halves of 16 KB)
-    __device__ __forceinline__ void store(uint32_t dst, int w, int lane) const {
-        const int d = dim0(lane), ch = (d & 63) / 8;
+    // Rows at or past n, and rows of the blocks in `missing`, become zeros.
+    __device__ __forceinline__ void blank(int n, uint32_t missing, int lane) {
+        const int r0 = first(lane);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const int t = j * RPS + row0(w, lane);
-            uint4 lo, hi;
-            convert16<T, kRow>(c[j], kRow ? b[j] : 127, lo, hi);
-            const uint32_t row = dst + (uint32_t)((d >> 6) * 16384 + t * 128);
+            const int r = r0 + (j ^ odd(lane));
+            if (r >= n || ((missing >> (r / BS)) & 1u)) {
+                c[j] = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kRow) sb[j / 4] = (sb[j / 4] & ~(0xffu << (8 * (j % 4)))) | (127u << (8 * (j % 4)));
+            }
+        }
+    }
+
+    __device__ __forceinline__ int byte(int j) const { return (int)((sb[j / 4] >> (8 * (j % 4))) & 0xffu); }
+
+    // into rows row0 .. row0 + 31 of the swizzled tile at shared address dst
+    // (64-dim halves of 16 KB)
+    __device__ __forceinline__ void store(uint32_t dst, int row0, int lane) const {
+        using P = PairScale<T>;
+        const int d = dim0(lane), ch = (d & 63) / 8;
+        const uint32_t half = dst + (uint32_t)(d >> 6) * 16384u;
+        auto put = [&](int j, const uint4& lo, const uint4& hi) {
+            const int t = row0 + first(lane) + (j ^ odd(lane));
+            const uint32_t row = half + t * 128;
             sts128(row + (((uint32_t)ch ^ (t & 7)) << 4), lo);
             sts128(row + (((uint32_t)(ch + 1) ^ (t & 7)) << 4), hi);
+        };
+        bool plain = true;
+        if constexpr (kRow) {
+            uint32_t far = 0;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) far = max(far, (uint32_t)(byte(j) - P::LO));
+            plain = __all_sync(0xffffffffu, far <= (uint32_t)(P::HI - P::LO));
+        }
+        if (plain) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                uint4 lo, hi;
+                convert16<T, kRow>(c[j], P::of(kRow ? byte(j) : 127), lo, hi);
+                put(j, lo, hi);
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < NJ; ++j) {
+                uint4 x = c[0];
+                int b = byte(0);
+#pragma unroll
+                for (int k = 1; k < NJ; ++k)
+                    if (k == j) { x = c[k]; b = byte(k); }
+                const bool in = b >= P::LO && b <= P::HI;
+                uint4 lo, hi;
+                convert16<T, kRow>(x, in ? P::of(b) : P::first(b), lo, hi);
+                const uint32_t m2 = in ? P::kHalf ? 0x3c003c00u : 0x3f803f80u : P::second(b);
+                uint32_t* o[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) *o[k] = P::kHalf ? mul_f16x2(*o[k], m2) : mul_bf16x2(*o[k], m2);
+                put(j, lo, hi);
+            }
         }
     }
 };

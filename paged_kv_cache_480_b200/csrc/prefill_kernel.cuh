@@ -91,13 +91,14 @@ struct PrefillParams {
 #define PKV_PREFILL_VST128 2
 #endif
 
-template <typename T, int D, int BS>
+template <typename T, typename TC, int D, int BS>
 struct PrefillShape {
+    static constexpr bool kConvert = !std::is_same<T, TC>::value;   // E4M3 caches
     static constexpr int M = 128;               // rows per query tile
     static constexpr int N = 128;               // keys per tile
     static constexpr int DH = D / 64;           // 64-dim halves (one 128-byte swizzle row each)
     static constexpr int BPT = N / BS;          // cache blocks per key tile
-    static constexpr int KST = D == 64 ? 4 : PKV_PREFILL_KST128;   // K stages
+    static constexpr int KST = D == 64 ? 4 : kConvert ? 2 : PKV_PREFILL_KST128;   // K stages
     static constexpr int VST = D == 64 ? 4 : PKV_PREFILL_VST128;   // V stages
     static constexpr int IR = 2;                // items in flight between the roles (one ahead: a deeper
                                                 // ring lets CTAs claim items further ahead, spreading
@@ -108,8 +109,10 @@ struct PrefillShape {
     static constexpr uint32_t KV_BYTES = DH * KV_HALF;      // K or V of one key tile
     static constexpr uint32_t OFF_K = 2 * Q_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + KST * KV_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_V + VST * KV_BYTES;
-    static constexpr uint32_t NBAR = 2 * IR + 4 + 2 * (KST + VST) + 10;
+    static constexpr uint32_t OFF_STG = OFF_V + VST * KV_BYTES;     // E4M3 caches: 4 warps x (K slot, V slot)
+    static constexpr uint32_t STG_SLOT = kConvert ? 32 / BS * cache_tile_bytes<TC>(D, BS) : 0;
+    static constexpr uint32_t OFF_BAR = OFF_STG + 8 * STG_SLOT;
+    static constexpr uint32_t NBAR = 2 * IR + 4 + 2 * (KST + VST) + 10 + (kConvert ? 8 : 0);
     static constexpr uint32_t OFF_ITEMS = (OFF_BAR + 8 * NBAR + 63) / 64 * 64;   // item ring, 64 bytes a slot
     static constexpr uint32_t OFF_HOLD = OFF_ITEMS + 64 * IR;                   // tensor-memory address
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;  // 1 KB alignment slack
@@ -143,12 +146,12 @@ template <typename T, typename TC, int D, int BS>
 __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     paged_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-    using S = PrefillShape<T, D, BS>;
+    using S = PrefillShape<T, TC, D, BS>;
     using namespace tcsm;
     constexpr int KST = S::KST, VST = S::VST, IR = S::IR;
     constexpr int N = S::N;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr bool kConvert = !std::is_same<T, TC>::value;
+    constexpr bool kConvert = S::kConvert;
     constexpr uint32_t kFullArrivals = kConvert ? 4 : 1;   // the converting warps, or the TMA thread
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_s = smem_addr(smem_raw);
@@ -179,6 +182,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     auto bar_ofree = [&](int x) { return bar + 8 * (B0 + 6 + x); };  // O_x written out (128 arrivals)
     const uint32_t bar_vz = bar + 8 * (B0 + 8);
     const uint32_t bar_fin = bar + 8 * (B0 + 9);
+    auto bar_stg = [&](int w, int v) { return bar + 8 * (B0 + 10 + 2 * w + v); };   // E4M3: a staging slot filled
     PrefillItem* items = reinterpret_cast<PrefillItem*>(smem + S::OFF_ITEMS);
     uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + S::OFF_HOLD);
     // warps 0-7, and warp 8 and the K/V producers (9 and 10, or 12-15) once each
@@ -208,6 +212,8 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
         }
         mbar_init(bar_vz, 1);
         mbar_init(bar_fin, 1);
+        if constexpr (kConvert)
+            for (int k = 0; k < 8; ++k) mbar_init(bar_stg(k >> 1, k & 1), 1);
         fence_mbar_init();
     }
     if (threadIdx.x == 32) {
@@ -340,50 +346,109 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     } else if (kConvert && warp >= 9) {
         // ===================== converting producers: warps 12-15, K and V =====================
         if constexpr (kConvert) {
-            const int w = warp - 12;
-            int jt = 0;                              // key tiles converted so far
-            bool ok = true;
-            TileCodes<T, TC, D, BS> kt, vt;
-            for (int j = 0; ok && w >= 0; ++j) {
+            if (warp >= 12) {
+                using Slice = SliceCodes<T, TC, D, BS>;
+                constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
+                static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
+                const int w = warp - 12;
+                const uint32_t slot[2] = {sm + S::OFF_STG + (2 * w) * S::STG_SLOT,
+                                          sm + S::OFF_STG + (2 * w + 1) * S::STG_SLOT};
+                bool ok = true;
+                int jt = 0, copies[2] = {0, 0};      // key tiles converted; copies requested into each slot
+                // the tile whose copies are requested next
                 PrefillItem it;
-                if (!take_item(j, it)) { ok = false; break; }
-                if (it.s < 0) break;
-                const int s = it.s, g = it.g;
-                const int nT = max(it.nT0, it.nT1);
-                const int nblk = (it.L + BS - 1) / BS;
-                auto tile_blocks = [&](int t) -> int {
-                    int phys = -1;
-                    const int lb = t * S::BPT + lane;
-                    if (lane < S::BPT && lb < nblk) {
-                        phys = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
-                        if (phys >= p.num_blocks) phys = -1;
-                        if (phys < 0 && w == 0) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                    }
-                    return phys;
+                int j = 0, t = 0, nT = 0, ids = -1;
+                int phys[BPW];
+                uint32_t missing = 0;
+                bool more = true;
+                auto begin_item = [&]() {
+                    more = take_item(j, it);
+                    if (!more) { ok = false; return; }
+                    more = it.s >= 0;
+                    t = 0;
+                    nT = max(it.nT0, it.nT1);
                 };
-                // K and V alternate; each stream's next tile is on its way from
-                // global memory while the other's is converted
-                int tbl = tile_blocks(0);
-                kt.load(p.k_cache, tbl, Hkv, g, it.L, w, lane);
-                for (int t = 0; t < nT; ++t, ++jt) {
-                    const int next = t + 1 < nT ? tile_blocks(t + 1) : -1;
-                    vt.load(p.v_cache, tbl, Hkv, g, it.L - t * N, w, lane);
-                    const int sk = jt % KST, sv = jt % VST;
-                    if (jt >= KST && !warp_wait(bar_kempty(sk), ((jt / KST) - 1) & 1, wl)) { ok = false; break; }
-                    kt.store(k_base(sk), w, lane);
-                    fence_proxy_async();             // before the tensor core reads the tile
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_kfull(sk));
-                    if (t + 1 < nT) kt.load(p.k_cache, next, Hkv, g, it.L - (t + 1) * N, w, lane);
-                    if (jt >= VST && !warp_wait(bar_vempty(sv), ((jt / VST) - 1) & 1, wl)) { ok = false; break; }
-                    vt.store(v_base(sv), w, lane);
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_vfull(sv));
-                    tbl = next;
+                // the blocks of tile t's slice; lane l holds the id of block l % BPW
+                // of the slice of tile l / BPW of a run of TPE tiles
+                auto find_blocks = [&]() {
+                    const int nblk = (it.L + BS - 1) / BS;
+                    if (t % TPE == 0) {
+                        const int lb = (t + lane / BPW) * S::BPT + w * BPW + lane % BPW;
+                        ids = -1;
+                        if (lb < nblk) {
+                            ids = __ldg(p.block_tables + (size_t)it.s * p.max_blocks_per_seq + lb);
+                            if (ids < 0 || ids >= p.num_blocks) {
+                                ids = -1;
+                                flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                            }
+                        }
+                    }
+                    missing = 0;
+#pragma unroll
+                    for (int i = 0; i < BPW; ++i) {
+                        phys[i] = __shfl_sync(kAll, ids, (t % TPE) * BPW + i);
+                        if (phys[i] < 0) missing |= 1u << i;
+                    }
+                };
+                auto request = [&](int v) {
+                    if (lane == 0) {
+                        uint32_t n = 0;
+#pragma unroll
+                        for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
+                        mbar_arrive_expect_tx(bar_stg(w, v), n);
+#pragma unroll
+                        for (int i = 0; i < BPW; ++i)
+                            if (phys[i] >= 0)
+                                bulk_g2s(slot[v] + i * Slice::TILE,
+                                         (v ? p.v_cache : p.k_cache) + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE,
+                                         Slice::TILE, bar_stg(w, v));
+                    }
+                    ++copies[v];
+                };
+                begin_item();
+                if (more) {
+                    find_blocks();
+                    request(0);
+                    request(1);
                 }
+                while (more && ok) {
+                    const int rows = it.L - t * N - 32 * w;       // of this slice
+                    const uint32_t gone = missing;
+                    const bool whole = rows >= 32 && gone == 0;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        Slice x;
+                        if (!warp_wait(bar_stg(w, v), (copies[v] - 1) & 1, wl)) { ok = false; break; }
+                        x.load(slot[v], lane);
+                        __syncwarp();                // every lane has its codes: the slot is free
+                        if (v == 0) {
+                            if (++t == nT) {
+                                ++j;
+                                begin_item();
+                                if (!ok) break;
+                            }
+                            if (more) find_blocks();
+                        }
+                        if (more) request(v);
+                        if (!whole) x.blank(rows, gone, lane);
+                        const int nst = v ? VST : KST, st = jt % nst;
+                        if (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
+                            ok = false;
+                            break;
+                        }
+                        x.store(v ? v_base(st) : k_base(st), 32 * w, lane);
+                        fence_proxy_async();         // before the tensor core reads the tile
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
+                    }
+                    ++jt;
+                }
+                if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+                // the copies still in flight land before this warp leaves
+                for (int v = 0; v < 2; ++v)
+                    if (copies[v] > 0) mbar_wait_bounded(bar_stg(w, v), (copies[v] - 1) & 1, kWaitLimit);
+                __syncwarp();
             }
-            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
         }
     } else if (!kConvert && warp >= 9) {
         // ===================== TMA producers: warp 9 K, warp 10 V =====================
