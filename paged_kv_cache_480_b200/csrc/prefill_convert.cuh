@@ -87,106 +87,108 @@ struct PairScale {
 
 // One warp's 32 rows of a 128-key tile: bulk copies bring them from their
 // blocks into the warp's own staging slot (each block's rows, then its scale
-// bytes), the warp takes them into registers, requests its rows of the next
-// tile into the same slot, and converts.  A lane holds NJ pieces of 16 codes
-// of neighbouring rows.  Pieces are dealt so that the eight lanes of a
-// shared-memory phase touch eight different 16-byte columns, both reading the
-// slot (two rows of opposite halves, or of opposite parity for 64 dims) and
-// writing the swizzled tile (rows of opposite parity).
+// bytes); the warp converts them piece by piece (16 codes of a row) into the
+// swizzled tile.  A lane takes NJ pieces of neighbouring rows, dealt so that
+// the eight lanes of a shared-memory phase touch eight different 16-byte
+// columns, both reading the slot (two rows of opposite halves, or of opposite
+// parity for 64 dims) and writing the tile (rows of opposite parity).
+//
+// The loop over pieces is rolled on purpose: unrolled, the code of a tile runs
+// once a tile and comes from beyond the instruction caches every time.
 template <typename T, typename TC, int D, int BS>
-struct SliceCodes {
+struct SliceConverter {
     static constexpr int ROWS = 32;
     static constexpr int BLOCKS = ROWS / BS;            // blocks of a slice
     static constexpr int TILE = cache_tile_bytes<TC>(D, BS);
     static constexpr int SLOT = BLOCKS * TILE;          // staging bytes
-    static constexpr int NJ = D / 16;                   // pieces (rows) a lane holds
+    static constexpr int NJ = D / 16;                   // pieces (rows) a lane takes
     static constexpr bool kRow = kRowScaled<TC>;
+    using P = PairScale<T>;
     static_assert(D == 64 || D == 128, "head size");
     static_assert(BLOCKS * BS == ROWS && BS % NJ == 0, "a lane's rows lie in one block");
 
-    uint4 c[NJ];
-    uint32_t sb[NJ / 4];                                // their scale bytes, in the order of c
+    int odd;            // piece j is row r0 + (j ^ odd) of the slice
+    int r0;
+    uint32_t src, sca;  // the lane's codes and scale bytes, from the slot's start
+    uint32_t dst;       // its row r0 of the tile, from the tile's start
+    uint32_t ch;        // first of the piece's two 16-byte columns
 
-    __device__ __forceinline__ static int odd(int lane) { return (lane >> 2) & 1; }
-    // first of the lane's NJ rows; piece j is row first + (j ^ odd)
-    __device__ __forceinline__ static int first(int lane) {
-        return NJ * (D == 128 ? odd(lane) | ((lane >> 4) << 1) : lane >> 2);
-    }
-    __device__ __forceinline__ static int dim0(int lane) {
-        return (lane & 3) * 16 + (D == 128 ? 64 * (((lane >> 3) & 1) ^ odd(lane)) : 0);
+    __device__ __forceinline__ SliceConverter(int w, int lane) {
+        odd = (lane >> 2) & 1;
+        r0 = NJ * (D == 128 ? odd | ((lane >> 4) << 1) : lane >> 2);
+        const int d = (lane & 3) * 16 + (D == 128 ? 64 * (((lane >> 3) & 1) ^ odd) : 0);
+        src = (r0 / BS) * TILE + (r0 % BS) * D + d;
+        sca = (r0 / BS) * TILE + BS * D + r0 % BS;
+        dst = (uint32_t)(d >> 6) * 16384u + (32 * w + r0) * 128;
+        ch = (d & 63) / 8;
     }
 
-    __device__ __forceinline__ void load(uint32_t slot, int lane) {
-        const int r0 = first(lane);
-        const uint32_t base = slot + (r0 / BS) * TILE;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) c[j] = lds128(base + (r0 % BS + (j ^ odd(lane))) * D + dim0(lane));
+    __device__ __forceinline__ static int lds8(uint32_t addr) {
+        uint32_t v;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+        return (int)v;
+    }
+
+    __device__ __forceinline__ void put(uint32_t tile, int u, const uint4& lo, const uint4& hi) const {
+        const uint32_t row = tile + dst + u * 128, t = (r0 + u) & 7;
+        sts128(row + ((ch ^ t) << 4), lo);
+        sts128(row + (((ch + 1) ^ t) << 4), hi);
+    }
+
+    // The slot at shared address `slot` into the tile at `tile`; rows at or past
+    // n, and rows of the blocks in `missing`, become zeros.
+    __device__ __forceinline__ void run(uint32_t slot, uint32_t tile, int n, uint32_t missing, int lane) const {
+        bool plain = n >= ROWS && missing == 0;
         if constexpr (kRow) {
-#pragma unroll
-            for (int k = 0; k < NJ / 4; ++k) {
-                sb[k] = (uint32_t)lds32(base + BS * D + r0 % BS + 4 * k);
-                if (odd(lane)) sb[k] = __byte_perm(sb[k], 0, 0x2301);
-            }
-        }
-    }
-
-    // Rows at or past n, and rows of the blocks in `missing`, become zeros.
-    __device__ __forceinline__ void blank(int n, uint32_t missing, int lane) {
-        const int r0 = first(lane);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int r = r0 + (j ^ odd(lane));
-            if (r >= n || ((missing >> (r / BS)) & 1u)) {
-                c[j] = make_uint4(0u, 0u, 0u, 0u);
-                if constexpr (kRow) sb[j / 4] = (sb[j / 4] & ~(0xffu << (8 * (j % 4)))) | (127u << (8 * (j % 4)));
-            }
-        }
-    }
-
-    __device__ __forceinline__ int byte(int j) const { return (int)((sb[j / 4] >> (8 * (j % 4))) & 0xffu); }
-
-    // into rows row0 .. row0 + 31 of the swizzled tile at shared address dst
-    // (64-dim halves of 16 KB)
-    __device__ __forceinline__ void store(uint32_t dst, int row0, int lane) const {
-        using P = PairScale<T>;
-        const int d = dim0(lane), ch = (d & 63) / 8;
-        const uint32_t half = dst + (uint32_t)(d >> 6) * 16384u;
-        auto put = [&](int j, const uint4& lo, const uint4& hi) {
-            const int t = row0 + first(lane) + (j ^ odd(lane));
-            const uint32_t row = half + t * 128;
-            sts128(row + (((uint32_t)ch ^ (t & 7)) << 4), lo);
-            sts128(row + (((uint32_t)(ch + 1) ^ (t & 7)) << 4), hi);
-        };
-        bool plain = true;
-        if constexpr (kRow) {
-            uint32_t far = 0;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) far = max(far, (uint32_t)(byte(j) - P::LO));
-            plain = __all_sync(0xffffffffu, far <= (uint32_t)(P::HI - P::LO));
+            // lane r looks at row r's scale
+            const uint32_t far = (uint32_t)(lds8(slot + (lane / BS) * TILE + BS * D + lane % BS) - P::LO);
+            plain = __all_sync(0xffffffffu, far <= (uint32_t)(P::HI - P::LO)) && plain;
         }
         if (plain) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
+            uint4 a = lds128(slot + src + odd * D), b = lds128(slot + src + (1 ^ odd) * D);
+            int sa = 127, sb = 127;
+            if constexpr (kRow) {
+                sa = lds8(slot + sca + odd);
+                sb = lds8(slot + sca + (1 ^ odd));
+            }
+#pragma unroll 1
+            for (int j = 0; j < NJ; j += 2) {
+                const uint4 ca = a, cb = b;
+                const uint32_t ma = P::of(sa), mb = P::of(sb);
+                if (j + 2 < NJ) {
+                    a = lds128(slot + src + ((j + 2) ^ odd) * D);
+                    b = lds128(slot + src + ((j + 3) ^ odd) * D);
+                    if constexpr (kRow) {
+                        sa = lds8(slot + sca + ((j + 2) ^ odd));
+                        sb = lds8(slot + sca + ((j + 3) ^ odd));
+                    }
+                }
                 uint4 lo, hi;
-                convert16<T, kRow>(c[j], P::of(kRow ? byte(j) : 127), lo, hi);
-                put(j, lo, hi);
+                convert16<T, kRow>(ca, ma, lo, hi);
+                put(tile, j ^ odd, lo, hi);
+                convert16<T, kRow>(cb, mb, lo, hi);
+                put(tile, (j + 1) ^ odd, lo, hi);
             }
         } else {
 #pragma unroll 1
             for (int j = 0; j < NJ; ++j) {
-                uint4 x = c[0];
-                int b = byte(0);
-#pragma unroll
-                for (int k = 1; k < NJ; ++k)
-                    if (k == j) { x = c[k]; b = byte(k); }
+                const int u = j ^ odd;
+                uint4 c = lds128(slot + src + u * D);
+                int b = kRow ? lds8(slot + sca + u) : 127;
+                if (r0 + u >= n || ((missing >> ((r0 + u) / BS)) & 1u)) {
+                    c = make_uint4(0u, 0u, 0u, 0u);
+                    b = 127;
+                }
                 const bool in = b >= P::LO && b <= P::HI;
                 uint4 lo, hi;
-                convert16<T, kRow>(x, in ? P::of(b) : P::first(b), lo, hi);
-                const uint32_t m2 = in ? P::kHalf ? 0x3c003c00u : 0x3f803f80u : P::second(b);
-                uint32_t* o[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+                convert16<T, kRow>(c, in ? P::of(b) : P::first(b), lo, hi);
+                if constexpr (kRow) {
+                    const uint32_t m2 = in ? P::kHalf ? 0x3c003c00u : 0x3f803f80u : P::second(b);
+                    uint32_t* o[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) *o[k] = P::kHalf ? mul_f16x2(*o[k], m2) : mul_bf16x2(*o[k], m2);
-                put(j, lo, hi);
+                    for (int k = 0; k < 8; ++k) *o[k] = P::kHalf ? mul_f16x2(*o[k], m2) : mul_bf16x2(*o[k], m2);
+                }
+                put(tile, u, lo, hi);
             }
         }
     }

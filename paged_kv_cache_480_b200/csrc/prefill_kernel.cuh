@@ -347,14 +347,16 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
         // ===================== converting producers: warps 12-15, K and V =====================
         if constexpr (kConvert) {
             if (warp >= 12) {
-                using Slice = SliceCodes<T, TC, D, BS>;
+                using Slice = SliceConverter<T, TC, D, BS>;
                 constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
                 static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
                 const int w = warp - 12;
-                const uint32_t slot[2] = {sm + S::OFF_STG + (2 * w) * S::STG_SLOT,
-                                          sm + S::OFF_STG + (2 * w + 1) * S::STG_SLOT};
+                const Slice conv(w, lane);
+                auto slot = [&](int v) { return sm + S::OFF_STG + (2 * w + v) * S::STG_SLOT; };   // 0: K, 1: V
                 bool ok = true;
-                int jt = 0, copies[2] = {0, 0};      // key tiles converted; copies requested into each slot
+                int jt = 0;                          // key tiles converted
+                int asked = 0;                       // key tiles found so far
+                int copies_k = 0, copies_v = 0;      // copies requested into each slot
                 // the tile whose copies are requested next
                 PrefillItem it;
                 int j = 0, t = 0, nT = 0, ids = -1;
@@ -396,57 +398,57 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
 #pragma unroll
                         for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
                         mbar_arrive_expect_tx(bar_stg(w, v), n);
+                        const unsigned char* cache = v ? p.v_cache : p.k_cache;
 #pragma unroll
                         for (int i = 0; i < BPW; ++i)
                             if (phys[i] >= 0)
-                                bulk_g2s(slot[v] + i * Slice::TILE,
-                                         (v ? p.v_cache : p.k_cache) + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE,
-                                         Slice::TILE, bar_stg(w, v));
+                                bulk_g2s(slot(v) + i * Slice::TILE,
+                                         cache + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE, Slice::TILE,
+                                         bar_stg(w, v));
                     }
-                    ++copies[v];
+                    if (v) ++copies_v; else ++copies_k;
                 };
                 begin_item();
                 if (more) {
                     find_blocks();
                     request(0);
                     request(1);
+                    asked = 1;
                 }
-                while (more && ok) {
+                for (; jt < asked && ok; ++jt) {
                     const int rows = it.L - t * N - 32 * w;       // of this slice
                     const uint32_t gone = missing;
-                    const bool whole = rows >= 32 && gone == 0;
-#pragma unroll
+#pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
-                        Slice x;
-                        if (!warp_wait(bar_stg(w, v), (copies[v] - 1) & 1, wl)) { ok = false; break; }
-                        x.load(slot[v], lane);
-                        __syncwarp();                // every lane has its codes: the slot is free
+                        const int nst = v ? VST : KST, st = jt % nst;
+                        if (!warp_wait(bar_stg(w, v), jt & 1, wl) ||
+                            (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
+                            ok = false;
+                            break;
+                        }
+                        conv.run(slot(v), v ? v_base(st) : k_base(st), rows, gone, lane);
+                        fence_proxy_async();         // before the tensor core reads the tile
+                        __syncwarp();                // (and every lane is done with the slot)
+                        if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
+                        // the slot's next tile, which may be the next item's first
                         if (v == 0) {
                             if (++t == nT) {
                                 ++j;
                                 begin_item();
                                 if (!ok) break;
                             }
-                            if (more) find_blocks();
+                            if (more) {
+                                find_blocks();
+                                ++asked;
+                            }
                         }
                         if (more) request(v);
-                        if (!whole) x.blank(rows, gone, lane);
-                        const int nst = v ? VST : KST, st = jt % nst;
-                        if (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
-                            ok = false;
-                            break;
-                        }
-                        x.store(v ? v_base(st) : k_base(st), 32 * w, lane);
-                        fence_proxy_async();         // before the tensor core reads the tile
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
                     }
-                    ++jt;
                 }
                 if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-                // the copies still in flight land before this warp leaves
-                for (int v = 0; v < 2; ++v)
-                    if (copies[v] > 0) mbar_wait_bounded(bar_stg(w, v), (copies[v] - 1) & 1, kWaitLimit);
+                // copies still in flight land before this warp leaves
+                if (copies_k > 0) mbar_wait_bounded(bar_stg(w, 0), (copies_k - 1) & 1, kWaitLimit);
+                if (copies_v > 0) mbar_wait_bounded(bar_stg(w, 1), (copies_v - 1) & 1, kWaitLimit);
                 __syncwarp();
             }
         }
