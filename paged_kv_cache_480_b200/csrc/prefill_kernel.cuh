@@ -30,8 +30,8 @@
 //                      a context's end in its last block;
 //   warp 11            takes items from the counter, hands them to the other
 //                      roles through a ring in shared memory, and loads q.
-//   warps 12-15        E4M3 caches only, in place of warps 9 and 10: load the
-//                      codes of both streams and convert them (prefill_convert.cuh).
+//   warps 12-15, 16-19 E4M3 caches only, in place of warps 9 and 10: fetch the
+//                      codes of K and V and convert them (prefill_convert.cuh).
 // Per key tile i of N = 128 keys and query tile x, in tensor memory
 // columns [256x, 256x + 256): S_x (128 fp32 columns), P_x over the first 64
 // of them (16-bit pairs), O_x (D fp32 columns) after S_x:
@@ -116,6 +116,8 @@ struct PrefillShape {
     static constexpr uint32_t OFF_ITEMS = (OFF_BAR + 8 * NBAR + 63) / 64 * 64;   // item ring, 64 bytes a slot
     static constexpr uint32_t OFF_HOLD = OFF_ITEMS + 64 * IR;                   // tensor-memory address
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;  // 1 KB alignment slack
+    static constexpr int kSoftmaxRegs = 144, kSideRegs = 64;
+    static_assert(2 * kSoftmaxRegs + 3 * kSideRegs <= 5 * 96, "registers of the 640 threads at launch");
     static constexpr uint32_t TM_TILE = 256;                // columns per query tile
     static constexpr uint32_t TM_S = 0;                     // S (N fp32 columns); P over its first N/2
     static constexpr uint32_t TM_O = N;                     // O at columns N .. N + D
@@ -125,10 +127,15 @@ struct PrefillShape {
     static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM");
 };
 
-// An E4M3 cache takes a fourth warpgroup, whose warps convert the tiles (and
-// leaves the TMA warps 9 and 10 without work).
+// An E4M3 cache takes two more warpgroups, whose warps convert the tiles (and
+// leaves the TMA warps 9 and 10 without work).  Its 640 threads start with 96
+// registers each, too few for the softmax's rows; the warpgroups share the
+// CTA's 5 * 96 a thread out again as 2 * kSoftmaxRegs + 3 * kSideRegs.
 template <typename T, typename TC>
-constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 512;
+constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 640;
+
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // One work item as the scheduler hands it to the other roles.
 struct PrefillItem {
@@ -185,8 +192,8 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     auto bar_stg = [&](int w, int v) { return bar + 8 * (B0 + 10 + 2 * w + v); };   // E4M3: a staging slot filled
     PrefillItem* items = reinterpret_cast<PrefillItem*>(smem + S::OFF_ITEMS);
     uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + S::OFF_HOLD);
-    // warps 0-7, and warp 8 and the K/V producers (9 and 10, or 12-15) once each
-    constexpr int kItemReaders = kConvert ? 13 : 11;
+    // warps 0-7, and warp 8 and the K/V producers (9 and 10, or 12-19) once each
+    constexpr int kItemReaders = kConvert ? 17 : 11;
     if (threadIdx.x == 0) {
         for (int k = 0; k < IR; ++k) {
             mbar_init(bar_ifull(k), 1);
@@ -256,387 +263,377 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
         return true;
     };
 
-    if (warp == 11) {
-        // ===================== scheduler: items from the counter, q by TMA =====================
-        const int pairs = p.num_seqs * Hkv;
-        const int gp = min(p.sched_group, pairs);
-        const int per_group = gp * p.q_tiles;
-        const int n_items = pairs * p.q_tiles;
-        int idx = blockIdx.x, j = 0, qloads[2] = {0, 0};
-        bool ok = true;
-        auto next_index = [&]() {
-            int v = 0;
-            if (lane == 0) v = atomicAdd(p.sched, 1) + (int)gridDim.x;
-            idx = __shfl_sync(kAll, v, 0);
-        };
-        while (true) {
-            PrefillItem it;
-            it.s = -1;
-            if (idx < n_items) {
-                // groups of p.sched_group (sequence, KV head) pairs, one after the
-                // other; inside a group the tiles with most keys go first.  The
-                // host sizes groups so that a group's K/V fits in half of L2 while
-                // its query tiles read it.
-                const int grp = idx / per_group;
-                const int in_g = idx - grp * per_group;
-                const int g_pairs = min(gp, pairs - grp * gp);   // the last group may be smaller
-                const int tile = p.q_tiles - 1 - in_g / g_pairs;
-                const int rest = grp * gp + in_g % g_pairs;
-                const int s = rest / Hkv;
-                const int q0 = __ldg(p.query_start_loc + s);
-                const int n = __ldg(p.query_start_loc + s + 1) - q0;
-                const int L = __ldg(p.context_lens + s);
-                const int i0 = tile * CQ;
-                if (n < 0 || n > L || n > p.q_tiles * CQ || L > p.max_blocks_per_seq * BS || q0 < 0 ||
-                    q0 + n > p.num_tokens) {
-                    // a bad sequence is skipped (its rows are not written) and flagged
-                    if (lane == 0 && tile == p.q_tiles - 1) flag_error(p.errors, PKV_DEVERR_CONTEXT);
-                    next_index();
-                    continue;
-                }
-                if (i0 >= n) {                  // a query-tile pair past the sequence's queries
-                    next_index();
-                    continue;
-                }
-                it.s = s;
-                it.g = rest - s * Hkv;
-                it.q0 = q0;
-                it.n = n;
-                it.L = L;
-                it.i0 = i0;
-                // key tiles each query tile needs (0: the tile holds no query)
-                it.nT0 = (L - n + min(i0 + QT, n) + N - 1) / N;
-                it.nT1 = i0 + QT < n ? (L - n + min(i0 + CQ, n) + N - 1) / N : 0;
-                const int nT = max(it.nT0, it.nT1);
-                const int nblk = (L + BS - 1) / BS;
-                it.vz_r0 = L - (nT - 1) * N;
-                it.vz_r1 = min(nblk * BS - (nT - 1) * N, N);
-            }
-            // hand the item (or the end mark) to the other roles
-            const int k = j % IR;
-            if (j >= IR && !warp_wait(bar_iempty(k), ((j / IR) - 1) & 1, wl)) { ok = false; break; }
-            if (lane == 0) {
-                items[k] = it;
-                mbar_arrive(bar_ifull(k));          // release: the slot's contents before the arrival
-            }
-            __syncwarp();
-            ++j;
-            if (it.s < 0) break;
-            // q of the item's tiles, once the previous item's products with them are done
-            for (int x = 0; x < (it.nT1 > 0 ? 2 : 1); ++x) {
-                if (qloads[x] >= 1 && !warp_wait(bar_qempty(x), (qloads[x] - 1) & 1, wl)) { ok = false; break; }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar_qfull(x), (uint32_t)(S::DH * QROWS * 128));
-                    for (int dh = 0; dh < S::DH; ++dh)
-                        tc05::tma_load_3d(q_base(x) + dh * S::Q_HALF, &tm_q, dh * 64, it.g * G,
-                                          it.q0 + it.i0 + x * QT, bar_qfull(x));
-                }
-                ++qloads[x];
-            }
-            if (!ok) break;
-            next_index();
-        }
-        // (if a wait gave up here, the other roles' own bounded waits give up too)
-        if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-        // every q copy requested above lands before this warp leaves
-        if (lane == 0)
-            for (int x = 0; x < 2; ++x)
-                if (qloads[x] > 0) mbar_wait_bounded(bar_qfull(x), (qloads[x] - 1) & 1, kWaitLimit);
-        __syncwarp();
-    } else if (kConvert && warp >= 9) {
-        // ===================== converting producers: warps 12-15, K and V =====================
+    if (kConvert && warp >= 12) {
+        // ===================== converting producers: warps 12-15 K, warps 16-19 V =====================
         if constexpr (kConvert) {
-            if (warp >= 12) {
-                using Slice = SliceConverter<T, TC, D, BS>;
-                constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
-                static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
-                const int w = warp - 12;
-                const Slice conv(w, lane);
-                auto slot = [&](int v) { return sm + S::OFF_STG + (2 * w + v) * S::STG_SLOT; };   // 0: K, 1: V
-                bool ok = true;
-                int jt = 0;                          // key tiles converted
-                int asked = 0;                       // key tiles found so far
-                int copies_k = 0, copies_v = 0;      // copies requested into each slot
-                // the tile whose copies are requested next
-                PrefillItem it;
-                int j = 0, t = 0, nT = 0, ids = -1;
-                int phys[BPW];
-                uint32_t missing = 0;
-                bool more = true;
-                auto begin_item = [&]() {
-                    more = take_item(j, it);
-                    if (!more) { ok = false; return; }
-                    more = it.s >= 0;
-                    t = 0;
-                    nT = max(it.nT0, it.nT1);
-                };
-                // the blocks of tile t's slice; lane l holds the id of block l % BPW
-                // of the slice of tile l / BPW of a run of TPE tiles
-                auto find_blocks = [&]() {
-                    const int nblk = (it.L + BS - 1) / BS;
-                    if (t % TPE == 0) {
-                        const int lb = (t + lane / BPW) * S::BPT + w * BPW + lane % BPW;
-                        ids = -1;
-                        if (lb < nblk) {
-                            ids = __ldg(p.block_tables + (size_t)it.s * p.max_blocks_per_seq + lb);
-                            if (ids < 0 || ids >= p.num_blocks) {
-                                ids = -1;
-                                flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                            }
-                        }
-                    }
-                    missing = 0;
-#pragma unroll
-                    for (int i = 0; i < BPW; ++i) {
-                        phys[i] = __shfl_sync(kAll, ids, (t % TPE) * BPW + i);
-                        if (phys[i] < 0) missing |= 1u << i;
-                    }
-                };
-                auto request = [&](int v) {
-                    if (lane == 0) {
-                        uint32_t n = 0;
-#pragma unroll
-                        for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
-                        mbar_arrive_expect_tx(bar_stg(w, v), n);
-                        const unsigned char* cache = v ? p.v_cache : p.k_cache;
-#pragma unroll
-                        for (int i = 0; i < BPW; ++i)
-                            if (phys[i] >= 0)
-                                bulk_g2s(slot(v) + i * Slice::TILE,
-                                         cache + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE, Slice::TILE,
-                                         bar_stg(w, v));
-                    }
-                    if (v) ++copies_v; else ++copies_k;
-                };
-                begin_item();
-                if (more) {
-                    find_blocks();
-                    request(0);
-                    request(1);
-                    asked = 1;
-                }
-                for (; jt < asked && ok; ++jt) {
-                    const int rows = it.L - t * N - 32 * w;       // of this slice
-                    const uint32_t gone = missing;
-#pragma unroll 1
-                    for (int v = 0; v < 2; ++v) {
-                        const int nst = v ? VST : KST, st = jt % nst;
-                        if (!warp_wait(bar_stg(w, v), jt & 1, wl) ||
-                            (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
-                            ok = false;
-                            break;
-                        }
-                        conv.run(slot(v), v ? v_base(st) : k_base(st), rows, gone, lane);
-                        fence_proxy_async();         // before the tensor core reads the tile
-                        __syncwarp();                // (and every lane is done with the slot)
-                        if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
-                        // the slot's next tile, which may be the next item's first
-                        if (v == 0) {
-                            if (++t == nT) {
-                                ++j;
-                                begin_item();
-                                if (!ok) break;
-                            }
-                            if (more) {
-                                find_blocks();
-                                ++asked;
-                            }
-                        }
-                        if (more) request(v);
-                    }
-                }
-                if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-                // copies still in flight land before this warp leaves
-                if (copies_k > 0) mbar_wait_bounded(bar_stg(w, 0), (copies_k - 1) & 1, kWaitLimit);
-                if (copies_v > 0) mbar_wait_bounded(bar_stg(w, 1), (copies_v - 1) & 1, kWaitLimit);
-                __syncwarp();
-            }
-        }
-    } else if (!kConvert && warp >= 9) {
-        // ===================== TMA producers: warp 9 K, warp 10 V =====================
-        const bool is_v = warp == 10;
-        const int nst = is_v ? VST : KST;
-        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-        int jt = 0;                                  // key tiles streamed so far
-        bool ok = true;
-        // V rows of the pending tile past its context end, zeroed once it lands
-        int vz_jt = -1, vz_r0 = 0, vz_r1 = 0;
-        auto do_vz = [&]() {
-            const int st = vz_jt % VST;
-            if (warp_wait(bar_vfull(st), (vz_jt / VST) & 1, wl)) {
-                const int rows = vz_r1 - vz_r0;
-                for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
-                    const int dh = i / (rows * 8);
-                    const int rem = i - dh * rows * 8;
-                    *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
-                                              (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_vz);
-            } else {
-                ok = false;
-            }
-            vz_jt = -1;
-        };
-        for (int j = 0; ok; ++j) {
+            reg_dec<S::kSideRegs>();
+            using Slice = SliceConverter<T, TC, D, BS>;
+            constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
+            static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
+            const int w = (warp - 12) & 3, v = (warp - 12) >> 2;   // slice, stream (0: K, 1: V)
+            const Slice conv(w, lane);
+            const uint32_t slot = sm + S::OFF_STG + (2 * w + v) * S::STG_SLOT, landed = bar_stg(w, v);
+            const unsigned char* cache = v ? p.v_cache : p.k_cache;
+            const int nst = v ? VST : KST;
+            bool ok = true;
+            int jt = 0;                          // key tiles converted
+            int copies = 0;                      // copies requested into the slot
+            // the tile whose copies are requested next
             PrefillItem it;
-            if (!take_item(j, it)) { ok = false; break; }
-            if (it.s < 0) break;
-            const int s = it.s, g = it.g;
-            const int nT = max(it.nT0, it.nT1);
-            const int nblk = (it.L + BS - 1) / BS;
-            // cache row of block `lane` of key tile t (one coalesced load per tile,
-            // a tile ahead of its copies); past the sequence's blocks, or for a
-            // bad id, the row past the pool, which TMA fills with zeros
-            auto tile_row = [&](int t) -> int {
-                int row = p.cache_rows;
-                const int lb = t * S::BPT + lane;
-                if (lane < S::BPT && lb < nblk) {
-                    const int phys = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
-                    if (phys >= 0 && phys < p.num_blocks) row = (phys * Hkv + g) * BS;
-                    else if (!is_v) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                }
-                return row;
+            int j = 0, t = 0, nT = 0, ids = -1;
+            int phys[BPW];
+            uint32_t missing = 0;
+            bool more = true;
+            auto begin_item = [&]() {
+                more = take_item(j, it);
+                if (!more) { ok = false; return; }
+                more = it.s >= 0;
+                t = 0;
+                nT = max(it.nT0, it.nT1);
             };
-            int next_row = tile_row(0);
-            for (int t = 0; t < nT; ++t, ++jt) {
-                const int cur_row = next_row;
-                if (t + 1 < nT) next_row = tile_row(t + 1);
+            // the blocks of tile t's slice; lane l holds the id of block l % BPW
+            // of the slice of tile l / BPW of a run of TPE tiles
+            auto find_blocks = [&]() {
+                const int nblk = (it.L + BS - 1) / BS;
+                if (t % TPE == 0) {
+                    const int lb = (t + lane / BPW) * S::BPT + w * BPW + lane % BPW;
+                    ids = -1;
+                    if (lb < nblk) {
+                        ids = __ldg(p.block_tables + (size_t)it.s * p.max_blocks_per_seq + lb);
+                        if (ids < 0 || ids >= p.num_blocks) {
+                            ids = -1;
+                            flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                        }
+                    }
+                }
+                missing = 0;
+#pragma unroll
+                for (int i = 0; i < BPW; ++i) {
+                    phys[i] = __shfl_sync(kAll, ids, (t % TPE) * BPW + i);
+                    if (phys[i] < 0) missing |= 1u << i;
+                }
+            };
+            auto request = [&]() {
+                if (lane == 0) {
+                    uint32_t n = 0;
+#pragma unroll
+                    for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
+                    mbar_arrive_expect_tx(landed, n);
+#pragma unroll
+                    for (int i = 0; i < BPW; ++i)
+                        if (phys[i] >= 0)
+                            bulk_g2s(slot + i * Slice::TILE, cache + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE,
+                                     Slice::TILE, landed);
+                }
+                ++copies;
+            };
+            begin_item();
+            if (more) {
+                find_blocks();
+                request();
+            }
+            for (; jt < copies; ++jt) {
                 const int st = jt % nst;
-                // a pending zeroing happens before its stage is waited for again
-                if (is_v && vz_jt >= 0 && jt >= vz_jt + VST) do_vz();
-                if (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
+                if (!warp_wait(landed, jt & 1, wl) ||
+                    (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = is_v ? bar_vfull(st) : bar_kfull(st);
-                const uint32_t dst = is_v ? v_base(st) : k_base(st);
-                if (lane == 0) mbar_arrive_expect_tx(full, S::KV_BYTES);
-#pragma unroll
-                for (int bi = 0; bi < S::BPT; ++bi) {
-                    const int row = __shfl_sync(kAll, cur_row, bi);
-                    if (lane == 0)
-                        for (int dh = 0; dh < S::DH; ++dh)
-                            tc05::tma_load_2d(dst + dh * S::KV_HALF + bi * BS * 128, map, dh * 64, row, full);
+                conv.run(slot, v ? v_base(st) : k_base(st), it.L - t * N - 32 * w, missing, lane);
+                fence_proxy_async();             // before the tensor core reads the tile
+                __syncwarp();                    // (and every lane is done with the slot)
+                if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
+                // the slot's next tile, which may be the next item's first
+                if (++t == nT) {
+                    ++j;
+                    begin_item();
                 }
-                // the item's last key tile: V rows from the context end to the end
-                // of its last block hold whatever the pool holds there
-                if (is_v && t == nT - 1 && it.vz_r0 < it.vz_r1) {
-                    if (vz_jt >= 0) do_vz();
-                    vz_jt = jt;
-                    vz_r0 = it.vz_r0;
-                    vz_r1 = it.vz_r1;
+                if (more) {
+                    find_blocks();
+                    request();
                 }
             }
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+            // the last copy lands before this warp leaves
+            if (copies > 0) mbar_wait_bounded(landed, (copies - 1) & 1, kWaitLimit);
+            __syncwarp();
         }
-        if (is_v && vz_jt >= 0 && ok) do_vz();
-        if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-        if (lane == 0) {
-            // every copy requested above lands before this warp leaves (the last
-            // copy into each stage; earlier ones were consumed before their stage
-            // was refilled)
-            for (int t = max(0, jt - nst); t < jt; ++t)
-                mbar_wait_bounded(is_v ? bar_vfull(t % nst) : bar_kfull(t % nst), (t / nst) & 1, kWaitLimit);
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ===================== MMA issue (one thread) =====================
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = tc05::instr_desc(kBf16, 128, N, false, false);
-            constexpr uint32_t idesc_pv = tc05::instr_desc(kBf16, 128, D, false, true);
-            // operand descriptors of query tile 0 and stage 0; the start-address
-            // field (bits 0-13, address / 16) is advanced by plain addition
-            const uint64_t dq = tc05::smem_desc(q_base(0), 16, 1024);
-            const uint64_t dk = tc05::smem_desc(k_base(0), 16, 1024);
-            const uint64_t dv = tc05::smem_desc(v_base(0), S::KV_HALF, 1024);
+    } else if (warp >= 8) {
+        if constexpr (kConvert) reg_dec<S::kSideRegs>();
+        if (warp == 11) {
+            // ===================== scheduler: items from the counter, q by TMA =====================
+            const int pairs = p.num_seqs * Hkv;
+            const int gp = min(p.sched_group, pairs);
+            const int per_group = gp * p.q_tiles;
+            const int n_items = pairs * p.q_tiles;
+            int idx = blockIdx.x, j = 0, qloads[2] = {0, 0};
             bool ok = true;
-            int jt0 = 0, vzc = 0;                          // key tiles of earlier items; zeroings seen
-            int qx[2] = {0, 0}, px[2] = {0, 0}, ox[2] = {0, 0};   // q loads, P phases, items per tile
-            for (int j = 0; ok; ++j) {
-                if (!mbar_wait_bounded(bar_ifull(j % IR), (j / IR) & 1, wl)) { ok = false; break; }
-                const PrefillItem it = items[j % IR];
-                mbar_arrive(bar_iempty(j % IR));
+            auto next_index = [&]() {
+                int v = 0;
+                if (lane == 0) v = atomicAdd(p.sched, 1) + (int)gridDim.x;
+                idx = __shfl_sync(kAll, v, 0);
+            };
+            while (true) {
+                PrefillItem it;
+                it.s = -1;
+                if (idx < n_items) {
+                    // groups of p.sched_group (sequence, KV head) pairs, one after the
+                    // other; inside a group the tiles with most keys go first.  The
+                    // host sizes groups so that a group's K/V fits in half of L2 while
+                    // its query tiles read it.
+                    const int grp = idx / per_group;
+                    const int in_g = idx - grp * per_group;
+                    const int g_pairs = min(gp, pairs - grp * gp);   // the last group may be smaller
+                    const int tile = p.q_tiles - 1 - in_g / g_pairs;
+                    const int rest = grp * gp + in_g % g_pairs;
+                    const int s = rest / Hkv;
+                    const int q0 = __ldg(p.query_start_loc + s);
+                    const int n = __ldg(p.query_start_loc + s + 1) - q0;
+                    const int L = __ldg(p.context_lens + s);
+                    const int i0 = tile * CQ;
+                    if (n < 0 || n > L || n > p.q_tiles * CQ || L > p.max_blocks_per_seq * BS || q0 < 0 ||
+                        q0 + n > p.num_tokens) {
+                        // a bad sequence is skipped (its rows are not written) and flagged
+                        if (lane == 0 && tile == p.q_tiles - 1) flag_error(p.errors, PKV_DEVERR_CONTEXT);
+                        next_index();
+                        continue;
+                    }
+                    if (i0 >= n) {                  // a query-tile pair past the sequence's queries
+                        next_index();
+                        continue;
+                    }
+                    it.s = s;
+                    it.g = rest - s * Hkv;
+                    it.q0 = q0;
+                    it.n = n;
+                    it.L = L;
+                    it.i0 = i0;
+                    // key tiles each query tile needs (0: the tile holds no query)
+                    it.nT0 = (L - n + min(i0 + QT, n) + N - 1) / N;
+                    it.nT1 = i0 + QT < n ? (L - n + min(i0 + CQ, n) + N - 1) / N : 0;
+                    const int nT = max(it.nT0, it.nT1);
+                    const int nblk = (L + BS - 1) / BS;
+                    it.vz_r0 = L - (nT - 1) * N;
+                    it.vz_r1 = min(nblk * BS - (nT - 1) * N, N);
+                }
+                // hand the item (or the end mark) to the other roles
+                const int k = j % IR;
+                if (j >= IR && !warp_wait(bar_iempty(k), ((j / IR) - 1) & 1, wl)) { ok = false; break; }
+                if (lane == 0) {
+                    items[k] = it;
+                    mbar_arrive(bar_ifull(k));          // release: the slot's contents before the arrival
+                }
+                __syncwarp();
+                ++j;
                 if (it.s < 0) break;
-                const int nT0 = it.nT0, nT1 = it.nT1, nT = max(nT0, nT1);
-                const bool two = nT1 > 0;
-                const bool vz = !kConvert && it.vz_r0 < it.vz_r1;   // (converted tiles come with zeros there)
-                const int vz_x = nT0 == nT ? 0 : 1;            // the first product reading the last V tile
-                auto qk = [&](int x, int i) {                  // S_x = Q_x K_i^T
-                    const uint32_t d = tm + x * S::TM_TILE + S::TM_S;
-                    const uint64_t ad = dq + (uint64_t)((x * S::Q_BYTES) >> 4);
-                    const uint64_t bd = dk + (uint64_t)((((jt0 + i) % KST) * S::KV_BYTES) >> 4);
-                    // k-th 16-wide slice: +32 bytes inside a swizzle row, next half after 4
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t qoff = ((k >> 2) * S::Q_HALF + (k & 3) * 32) >> 4;
-                        const uint32_t koff = ((k >> 2) * S::KV_HALF + (k & 3) * 32) >> 4;
-                        tc05::mma_ss(d, ad + qoff, bd + koff, idesc_qk, k > 0 ? 1u : 0u);
+                // q of the item's tiles, once the previous item's products with them are done
+                for (int x = 0; x < (it.nT1 > 0 ? 2 : 1); ++x) {
+                    if (qloads[x] >= 1 && !warp_wait(bar_qempty(x), (qloads[x] - 1) & 1, wl)) { ok = false; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar_qfull(x), (uint32_t)(S::DH * QROWS * 128));
+                        for (int dh = 0; dh < S::DH; ++dh)
+                            tc05::tma_load_3d(q_base(x) + dh * S::Q_HALF, &tm_q, dh * 64, it.g * G,
+                                              it.q0 + it.i0 + x * QT, bar_qfull(x));
                     }
-                    tc05::commit(bar_s(x));
-                    if (i == (x ? nT1 : nT0) - 1) tc05::commit(bar_qempty(x));   // Q_x free for the next item
-                };
-                auto pv = [&](int x, int i) -> bool {          // O_x += P_x V_i
-                    const int jt = jt0 + i, sv = jt % VST;
-                    if (!mbar_wait_bounded(bar_vfull(sv), (jt / VST) & 1, wl)) return false;
-                    if (vz && i == nT - 1 && x == vz_x) {
-                        if (!mbar_wait_bounded(bar_vz, vzc & 1, wl)) return false;
-                        ++vzc;
-                    }
-                    if (!mbar_wait_bounded(bar_p(x), px[x] & 1, wl)) return false;
-                    ++px[x];
-                    if (i == 0) {
-                        // the tile's previous item must be written out before O_x restarts
-                        if (ox[x] >= 1 && !mbar_wait_bounded(bar_ofree(x), (ox[x] - 1) & 1, wl)) return false;
-                        ++ox[x];
-                    }
-                    tc05::fence_after_sync();
-                    const uint32_t base = tm + x * S::TM_TILE;
-                    const uint64_t vd = dv + (uint64_t)((sv * S::KV_BYTES) >> 4);
-                    // k-th 16 keys: 16 rows of 128 bytes further; P pairs 8 columns further
-#pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        tc05::mma_ts(base + S::TM_O, base + S::TM_S + 8 * k, vd + (uint64_t)(k * 128), idesc_pv,
-                                     (i > 0 || k > 0) ? 1u : 0u);
-                    if (i == (x ? nT1 : nT0) - 1) tc05::commit(bar_o(x));
-                    return true;
-                };
-                if (!mbar_wait_bounded(bar_qfull(0), qx[0] & 1, wl)) { ok = false; break; }
-                ++qx[0];
-                for (int i = 0; ok && i < nT; ++i) {
-                    const int jt = jt0 + i;
-                    if (!mbar_wait_bounded(bar_kfull(jt % KST), (jt / KST) & 1, wl)) { ok = false; break; }
-                    tc05::fence_after_sync();
-                    if (i < nT0) qk(0, i);
-                    if (two && i >= 1) {                       // V(i-1) last read by PV_1(i-1)
-                        if (!pv(1, i - 1)) { ok = false; break; }
-                        tc05::commit(bar_vempty((jt - 1) % VST));
-                    }
-                    if (i < nT1) {
-                        if (i == 0) {                           // q tile 1 is needed from here on
-                            if (!mbar_wait_bounded(bar_qfull(1), qx[1] & 1, wl)) { ok = false; break; }
-                            ++qx[1];
-                        }
-                        qk(1, i);
-                    }
-                    tc05::commit(bar_kempty(jt % KST));
-                    if (i < nT0) {
-                        if (!pv(0, i)) { ok = false; break; }
-                        if (!two) tc05::commit(bar_vempty(jt % VST));
-                    }
+                    ++qloads[x];
                 }
-                if (ok && two) {
-                    if (pv(1, nT - 1)) tc05::commit(bar_vempty((jt0 + nT - 1) % VST));
-                    else ok = false;
-                }
-                jt0 += nT;
+                if (!ok) break;
+                next_index();
             }
-            if (!ok) flag_error(p.errors, PKV_DEVERR_WAIT);
-            // every MMA issued above is complete before the tensor memory is freed
-            tc05::commit(bar_fin);
-            mbar_wait_bounded(bar_fin, 0, kWaitLimit);
+            // (if a wait gave up here, the other roles' own bounded waits give up too)
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+            // every q copy requested above lands before this warp leaves
+            if (lane == 0)
+                for (int x = 0; x < 2; ++x)
+                    if (qloads[x] > 0) mbar_wait_bounded(bar_qfull(x), (qloads[x] - 1) & 1, kWaitLimit);
+            __syncwarp();
+        } else if (warp == 8) {
+            // ===================== MMA issue (one thread) =====================
+            if (lane == 0) {
+                constexpr uint32_t idesc_qk = tc05::instr_desc(kBf16, 128, N, false, false);
+                constexpr uint32_t idesc_pv = tc05::instr_desc(kBf16, 128, D, false, true);
+                // operand descriptors of query tile 0 and stage 0; the start-address
+                // field (bits 0-13, address / 16) is advanced by plain addition
+                const uint64_t dq = tc05::smem_desc(q_base(0), 16, 1024);
+                const uint64_t dk = tc05::smem_desc(k_base(0), 16, 1024);
+                const uint64_t dv = tc05::smem_desc(v_base(0), S::KV_HALF, 1024);
+                bool ok = true;
+                int jt0 = 0, vzc = 0;                          // key tiles of earlier items; zeroings seen
+                int qx[2] = {0, 0}, px[2] = {0, 0}, ox[2] = {0, 0};   // q loads, P phases, items per tile
+                for (int j = 0; ok; ++j) {
+                    if (!mbar_wait_bounded(bar_ifull(j % IR), (j / IR) & 1, wl)) { ok = false; break; }
+                    const PrefillItem it = items[j % IR];
+                    mbar_arrive(bar_iempty(j % IR));
+                    if (it.s < 0) break;
+                    const int nT0 = it.nT0, nT1 = it.nT1, nT = max(nT0, nT1);
+                    const bool two = nT1 > 0;
+                    const bool vz = !kConvert && it.vz_r0 < it.vz_r1;   // (converted tiles come with zeros there)
+                    const int vz_x = nT0 == nT ? 0 : 1;            // the first product reading the last V tile
+                    auto qk = [&](int x, int i) {                  // S_x = Q_x K_i^T
+                        const uint32_t d = tm + x * S::TM_TILE + S::TM_S;
+                        const uint64_t ad = dq + (uint64_t)((x * S::Q_BYTES) >> 4);
+                        const uint64_t bd = dk + (uint64_t)((((jt0 + i) % KST) * S::KV_BYTES) >> 4);
+                        // k-th 16-wide slice: +32 bytes inside a swizzle row, next half after 4
+    #pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t qoff = ((k >> 2) * S::Q_HALF + (k & 3) * 32) >> 4;
+                            const uint32_t koff = ((k >> 2) * S::KV_HALF + (k & 3) * 32) >> 4;
+                            tc05::mma_ss(d, ad + qoff, bd + koff, idesc_qk, k > 0 ? 1u : 0u);
+                        }
+                        tc05::commit(bar_s(x));
+                        if (i == (x ? nT1 : nT0) - 1) tc05::commit(bar_qempty(x));   // Q_x free for the next item
+                    };
+                    auto pv = [&](int x, int i) -> bool {          // O_x += P_x V_i
+                        const int jt = jt0 + i, sv = jt % VST;
+                        if (!mbar_wait_bounded(bar_vfull(sv), (jt / VST) & 1, wl)) return false;
+                        if (vz && i == nT - 1 && x == vz_x) {
+                            if (!mbar_wait_bounded(bar_vz, vzc & 1, wl)) return false;
+                            ++vzc;
+                        }
+                        if (!mbar_wait_bounded(bar_p(x), px[x] & 1, wl)) return false;
+                        ++px[x];
+                        if (i == 0) {
+                            // the tile's previous item must be written out before O_x restarts
+                            if (ox[x] >= 1 && !mbar_wait_bounded(bar_ofree(x), (ox[x] - 1) & 1, wl)) return false;
+                            ++ox[x];
+                        }
+                        tc05::fence_after_sync();
+                        const uint32_t base = tm + x * S::TM_TILE;
+                        const uint64_t vd = dv + (uint64_t)((sv * S::KV_BYTES) >> 4);
+                        // k-th 16 keys: 16 rows of 128 bytes further; P pairs 8 columns further
+    #pragma unroll
+                        for (int k = 0; k < N / 16; ++k)
+                            tc05::mma_ts(base + S::TM_O, base + S::TM_S + 8 * k, vd + (uint64_t)(k * 128), idesc_pv,
+                                         (i > 0 || k > 0) ? 1u : 0u);
+                        if (i == (x ? nT1 : nT0) - 1) tc05::commit(bar_o(x));
+                        return true;
+                    };
+                    if (!mbar_wait_bounded(bar_qfull(0), qx[0] & 1, wl)) { ok = false; break; }
+                    ++qx[0];
+                    for (int i = 0; ok && i < nT; ++i) {
+                        const int jt = jt0 + i;
+                        if (!mbar_wait_bounded(bar_kfull(jt % KST), (jt / KST) & 1, wl)) { ok = false; break; }
+                        tc05::fence_after_sync();
+                        if (i < nT0) qk(0, i);
+                        if (two && i >= 1) {                       // V(i-1) last read by PV_1(i-1)
+                            if (!pv(1, i - 1)) { ok = false; break; }
+                            tc05::commit(bar_vempty((jt - 1) % VST));
+                        }
+                        if (i < nT1) {
+                            if (i == 0) {                           // q tile 1 is needed from here on
+                                if (!mbar_wait_bounded(bar_qfull(1), qx[1] & 1, wl)) { ok = false; break; }
+                                ++qx[1];
+                            }
+                            qk(1, i);
+                        }
+                        tc05::commit(bar_kempty(jt % KST));
+                        if (i < nT0) {
+                            if (!pv(0, i)) { ok = false; break; }
+                            if (!two) tc05::commit(bar_vempty(jt % VST));
+                        }
+                    }
+                    if (ok && two) {
+                        if (pv(1, nT - 1)) tc05::commit(bar_vempty((jt0 + nT - 1) % VST));
+                        else ok = false;
+                    }
+                    jt0 += nT;
+                }
+                if (!ok) flag_error(p.errors, PKV_DEVERR_WAIT);
+                // every MMA issued above is complete before the tensor memory is freed
+                tc05::commit(bar_fin);
+                mbar_wait_bounded(bar_fin, 0, kWaitLimit);
+            }
+        } else if constexpr (!kConvert) {
+            // ===================== TMA producers: warp 9 K, warp 10 V =====================
+            const bool is_v = warp == 10;
+            const int nst = is_v ? VST : KST;
+            const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+            int jt = 0;                                  // key tiles streamed so far
+            bool ok = true;
+            // V rows of the pending tile past its context end, zeroed once it lands
+            int vz_jt = -1, vz_r0 = 0, vz_r1 = 0;
+            auto do_vz = [&]() {
+                const int st = vz_jt % VST;
+                if (warp_wait(bar_vfull(st), (vz_jt / VST) & 1, wl)) {
+                    const int rows = vz_r1 - vz_r0;
+                    for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
+                        const int dh = i / (rows * 8);
+                        const int rem = i - dh * rows * 8;
+                        *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
+                                                  (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_vz);
+                } else {
+                    ok = false;
+                }
+                vz_jt = -1;
+            };
+            for (int j = 0; ok; ++j) {
+                PrefillItem it;
+                if (!take_item(j, it)) { ok = false; break; }
+                if (it.s < 0) break;
+                const int s = it.s, g = it.g;
+                const int nT = max(it.nT0, it.nT1);
+                const int nblk = (it.L + BS - 1) / BS;
+                // cache row of block `lane` of key tile t (one coalesced load per tile,
+                // a tile ahead of its copies); past the sequence's blocks, or for a
+                // bad id, the row past the pool, which TMA fills with zeros
+                auto tile_row = [&](int t) -> int {
+                    int row = p.cache_rows;
+                    const int lb = t * S::BPT + lane;
+                    if (lane < S::BPT && lb < nblk) {
+                        const int phys = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
+                        if (phys >= 0 && phys < p.num_blocks) row = (phys * Hkv + g) * BS;
+                        else if (!is_v) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                    }
+                    return row;
+                };
+                int next_row = tile_row(0);
+                for (int t = 0; t < nT; ++t, ++jt) {
+                    const int cur_row = next_row;
+                    if (t + 1 < nT) next_row = tile_row(t + 1);
+                    const int st = jt % nst;
+                    // a pending zeroing happens before its stage is waited for again
+                    if (is_v && vz_jt >= 0 && jt >= vz_jt + VST) do_vz();
+                    if (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = is_v ? bar_vfull(st) : bar_kfull(st);
+                    const uint32_t dst = is_v ? v_base(st) : k_base(st);
+                    if (lane == 0) mbar_arrive_expect_tx(full, S::KV_BYTES);
+    #pragma unroll
+                    for (int bi = 0; bi < S::BPT; ++bi) {
+                        const int row = __shfl_sync(kAll, cur_row, bi);
+                        if (lane == 0)
+                            for (int dh = 0; dh < S::DH; ++dh)
+                                tc05::tma_load_2d(dst + dh * S::KV_HALF + bi * BS * 128, map, dh * 64, row, full);
+                    }
+                    // the item's last key tile: V rows from the context end to the end
+                    // of its last block hold whatever the pool holds there
+                    if (is_v && t == nT - 1 && it.vz_r0 < it.vz_r1) {
+                        if (vz_jt >= 0) do_vz();
+                        vz_jt = jt;
+                        vz_r0 = it.vz_r0;
+                        vz_r1 = it.vz_r1;
+                    }
+                }
+            }
+            if (is_v && vz_jt >= 0 && ok) do_vz();
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+            if (lane == 0) {
+                // every copy requested above lands before this warp leaves (the last
+                // copy into each stage; earlier ones were consumed before their stage
+                // was refilled)
+                for (int t = max(0, jt - nst); t < jt; ++t)
+                    mbar_wait_bounded(is_v ? bar_vfull(t % nst) : bar_kfull(t % nst), (t / nst) & 1, kWaitLimit);
+            }
+            __syncwarp();
         }
     } else {
+        if constexpr (kConvert) reg_inc<S::kSoftmaxRegs>();
         // ===================== softmax and output: one row per thread =====================
         const int x = warp >> 2;                        // query tile
         const int wq = warp & 3;
