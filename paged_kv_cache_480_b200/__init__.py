@@ -29,5 +29,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)   # found at once from the next use on
+        return value
     raise AttributeError(name)

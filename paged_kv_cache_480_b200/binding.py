@@ -376,10 +376,83 @@ def fp8row_cache_shape(num_blocks, num_kv_heads, block_size, head_size):
     return num_blocks, num_kv_heads, block_size * (head_size + 1)
 
 
+# The calls below are issued once a layer and step, often for a few tokens, when
+# the host's time counts: they pass plain integers, and read each tensor's
+# device as its index.
+def _device(t, name):
+    """Index of the GPU that t is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _on(dev, t, name):
+    """Device pointer of a contiguous tensor on GPU dev."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the GPU of the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(dev, t, name):
+    """Device pointer of [T, heads, head_size] rows whose tokens may lie apart, and their stride."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the GPU of the other tensors")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: heads must be contiguous within a token")
+    # (a single token's stride may be anything: it is never applied)
+    return t.data_ptr(), st if T > 1 else H * D
+
+
+def _int64(dev, t, n, name):
+    if t.dtype != _torch().int64 or t.numel() != n:
+        raise TypeError(f"{name} must be int64 [{n}]")
+    return _on(dev, t, name)
+
+
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+        _DTYPE_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    return _torch_module
+
+
+_DTYPE_CODES = {}
+
+
+def _code(dtype):
+    _torch()
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _call(name, dev, stream, *args):
+    """One library call on GPU dev, its stream last; raises on a bad status."""
+    torch = _torch()
+    fn = getattr(_lib if _lib is not None else load_library(), name)
+    if torch._C._cuda_getDevice() != dev:       # launches go to the current device
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st != PKV_OK:
+        _check(st, name)
+
+
 def _row_caches(k_cache, v_cache, D):
     """(num_blocks, num_kv_heads, block_size) of a pair of row caches."""
-    import torch
-    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+    u8 = _torch().uint8
+    if k_cache.dtype != u8 or v_cache.dtype != u8:
         raise TypeError("row caches are uint8 (fp8row_cache_shape)")
     NB, Hkv, n = k_cache.shape
     if v_cache.shape != k_cache.shape or n % (D + 1):
@@ -387,91 +460,92 @@ def _row_caches(k_cache, v_cache, D):
     return NB, Hkv, n // (D + 1)
 
 
-def _rows(t, name):
-    """Device pointer of [T, heads, head_size] rows whose tokens may lie apart, and their stride."""
-    if t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
-        raise ValueError(f"{name}: heads must be contiguous within a token")
-    # (a single token's stride may be anything: it is never applied)
-    return _cuda(t, name), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _same_caches(k_cache, v_cache, D, dtype):
+    """The same of a pair of caches that hold elements of one type."""
+    NB, Hkv, bs, D2 = k_cache.shape
+    if D2 != D or v_cache.shape != k_cache.shape or k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size] of the rows' dtype")
+    return NB, Hkv, bs
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t.device != first.device:
-            raise ValueError("all tensors must be on one device")
-
-
-def _int64(t, n, name):
-    import torch
-    if t.dtype != torch.int64 or t.numel() != n:
-        raise TypeError(f"{name} must be int64 [{n}]")
-    return _contig(t, name)
+def _e4m3_caches(k_cache, v_cache, D):
+    """The same of a pair of E4M3 caches with one scale each."""
+    torch = _torch()
+    NB, Hkv, bs, D2 = k_cache.shape
+    if D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size]")
+    for t in (k_cache, v_cache):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError("the caches must hold E4M3 codes (uint8 or float8_e4m3fn)")
+    return NB, Hkv, bs
 
 
 def reshape_and_cache_fp8row(key, value, k_cache, v_cache, slot_mapping, stream=None):
     """Quantising cache write into 8-bit row caches (reshape_and_cache_fp8row in
     pagedkv.h): key/value [T, Hkv, D] in f32/f16/bf16, each (token, head) row
     with a scale of its own."""
-    lib = load_library()
     T, Hkv, D = key.shape
     NB, Hkv2, bs = _row_caches(k_cache, v_cache, D)
     if Hkv != Hkv2 or value.shape != key.shape or value.dtype != key.dtype:
         raise ValueError("key/value shape does not match the cache")
-    _same_device(key, value, k_cache, v_cache, slot_mapping)
-    kp, ks = _rows(key, "key")
-    vp, vs = _rows(value, "value")
-    st = lib.reshape_and_cache_fp8row(kp, vp, _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
-                                      _int64(slot_mapping, T, "slot_mapping"), T, Hkv, D, bs, NB, ks, vs,
-                                      _dtype_code(key), _stream(stream, key.device))
-    _check(st, "reshape_and_cache_fp8row")
+    dev = _device(key, "key")
+    kp, ks = _rows(dev, key, "key")
+    vp, vs = _rows(dev, value, "value")
+    _call("reshape_and_cache_fp8row", dev, stream, kp, vp, _on(dev, k_cache, "k_cache"), _on(dev, v_cache, "v_cache"),
+          _int64(dev, slot_mapping, T, "slot_mapping"), T, Hkv, D, bs, NB, ks, vs, _code(key.dtype))
 
 
 def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len=None,
                                   partition_size=0, workspace=None, stream=None):
     """Decode attention over 8-bit row caches (paged_attention_decode_fp8row in
     pagedkv.h): q, out [S, H, D] in f32/f16/bf16; caches of fp8row_cache_shape."""
-    import torch
-    lib = load_library()
+    int32 = _torch().int32
     S, H, D = q.shape
     NB, Hkv, bs = _row_caches(k_cache, v_cache, D)
     if out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out and q must share shape and dtype")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if block_tables.dtype != int32 or context_lens.dtype != int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if block_tables.shape[0] != S or context_lens.numel() != S:
+    S2, MB = block_tables.shape
+    if S2 != S or context_lens.numel() != S:
         raise ValueError("block_tables must be [S, MB] and context_lens [S]")
-    _same_device(q, out, k_cache, v_cache, block_tables, context_lens)
-    MB = block_tables.shape[1]
+    dev = _device(q, "q")
     if max_context_len is None:
         max_context_len = MB * bs
-    code = _dtype_code(q)
-    need = lib.paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
-    if need == 0:
-        raise PagedKVError(2, "paged_attention_workspace_size")
+    code = _code(q.dtype)
     if workspace is None:
+        need = load_library().paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
+        if need == 0:
+            raise PagedKVError(2, "paged_attention_workspace_size")
         workspace = default_workspace(q.device, need)
-    st = lib.paged_attention_decode_fp8row(
-        _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
-        _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"), float(scale), Hkv, bs, S, H, D,
-        NB, MB, int(max_context_len), code, int(partition_size), _cuda(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream, q.device))
-    _check(st, "paged_attention_decode_fp8row")
+    _call("paged_attention_decode_fp8row", dev, stream, _on(dev, out, "out"), _on(dev, q, "q"),
+          _on(dev, k_cache, "k_cache"), _on(dev, v_cache, "v_cache"), _on(dev, block_tables, "block_tables"),
+          _on(dev, context_lens, "context_lens"), scale, Hkv, bs, S, H, D, NB, MB, max_context_len, code,
+          partition_size, _on(dev, workspace, "workspace"), workspace.numel() * workspace.element_size())
     return out
 
 
-def _prefill_args(out, q, block_tables, context_lens, query_start_loc, max_query_len):
-    import torch
+def _prefill(name, caches, scales, out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+             max_query_len, stream):
+    int32 = _torch().int32
+    T, H, D = q.shape
+    NB, Hkv, bs = caches
     if out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out and q must share shape and dtype")
-    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
-            or query_start_loc.dtype != torch.int32):
+    if block_tables.dtype != int32 or context_lens.dtype != int32 or query_start_loc.dtype != int32:
         raise TypeError("block_tables, context_lens and query_start_loc must be int32")
     S = context_lens.numel()
-    if query_start_loc.numel() != S + 1 or block_tables.shape[0] != S:
+    S2, MB = block_tables.shape
+    if query_start_loc.numel() != S + 1 or S2 != S:
         raise ValueError("query_start_loc must be [S + 1] and block_tables [S, MB]")
     if max_query_len is None:
         raise ValueError("max_query_len is required (a host-known bound of the queries per sequence)")
-    return S
+    dev = _device(q, "q")
+    _call(name, dev, stream, _on(dev, out, "out"), _on(dev, q, "q"), _on(dev, k_cache, "k_cache"),
+          _on(dev, v_cache, "v_cache"), _on(dev, block_tables, "block_tables"),
+          _on(dev, context_lens, "context_lens"), _on(dev, query_start_loc, "query_start_loc"), scale, *scales, T, S,
+          H, Hkv, D, bs, NB, MB, max_query_len, _code(q.dtype))
+    return out
 
 
 def paged_attention_prefill_fp8row(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
@@ -479,18 +553,8 @@ def paged_attention_prefill_fp8row(out, q, k_cache, v_cache, block_tables, conte
     """Causal attention of prompts or chunks over 8-bit row caches
     (paged_attention_prefill_fp8row in pagedkv.h); arguments as for
     paged_attention_prefill, caches of fp8row_cache_shape."""
-    lib = load_library()
-    T, H, D = q.shape
-    NB, Hkv, bs = _row_caches(k_cache, v_cache, D)
-    S = _prefill_args(out, q, block_tables, context_lens, query_start_loc, max_query_len)
-    _same_device(q, out, k_cache, v_cache, block_tables, context_lens, query_start_loc)
-    st = lib.paged_attention_prefill_fp8row(
-        _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
-        _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"),
-        _contig(query_start_loc, "query_start_loc"), float(scale), T, S, H, Hkv, D, bs, NB,
-        block_tables.shape[1], int(max_query_len), _dtype_code(q), _stream(stream, q.device))
-    _check(st, "paged_attention_prefill_fp8row")
-    return out
+    return _prefill("paged_attention_prefill_fp8row", _row_caches(k_cache, v_cache, q.shape[2]), (), out, q, k_cache,
+                    v_cache, block_tables, context_lens, query_start_loc, scale, max_query_len, stream)
 
 
 def paged_attention_prefill_fp8kv(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
@@ -498,20 +562,8 @@ def paged_attention_prefill_fp8kv(out, q, k_cache, v_cache, block_tables, contex
     """Causal attention of prompts or chunks over FP8 E4M3 caches with one scale
     for K and one for V (paged_attention_prefill_fp8kv in pagedkv.h):
     k_cache / v_cache uint8 [NB, Hkv, bs, D]."""
-    lib = load_library()
-    T, H, D = q.shape
-    NB, Hkv, bs, D2 = k_cache.shape
-    if D2 != D or tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise ValueError("shape mismatch")
-    S = _prefill_args(out, q, block_tables, context_lens, query_start_loc, max_query_len)
-    _same_device(q, out, k_cache, v_cache, block_tables, context_lens, query_start_loc)
-    st = lib.paged_attention_prefill_fp8kv(
-        _contig(out, "out"), _contig(q, "q"), _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache"),
-        _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"),
-        _contig(query_start_loc, "query_start_loc"), float(scale), float(k_scale), float(v_scale), T, S, H, Hkv, D,
-        bs, NB, block_tables.shape[1], int(max_query_len), _dtype_code(q), _stream(stream, q.device))
-    _check(st, "paged_attention_prefill_fp8kv")
-    return out
+    return _prefill("paged_attention_prefill_fp8kv", _e4m3_caches(k_cache, v_cache, q.shape[2]), (k_scale, v_scale),
+                    out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, max_query_len, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -525,72 +577,66 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     """(inv_freq, attention_scale) of pkv_rotary_frequencies in pagedkv.h:
     inv_freq float32 [rotary_dim / 2] on the host, to be moved to the device
     once; scaling None, "linear", "base", "by_turns" or "by_index"."""
-    import torch
+    torch = _torch()
     if scaling not in ROTARY_SCALING:
         raise ValueError(f"scaling must be one of {list(ROTARY_SCALING)}")
     inv_freq = torch.empty(max(int(rotary_dim), 2) // 2, dtype=torch.float32)
     att = ctypes.c_float()
-    st = load_library().pkv_rotary_frequencies(ctypes.c_void_p(inv_freq.data_ptr()), ctypes.byref(att),
-                                               int(rotary_dim), float(base), ROTARY_SCALING[scaling], float(factor),
-                                               int(original_context), float(fast_turns), float(slow_turns))
+    st = load_library().pkv_rotary_frequencies(inv_freq.data_ptr(), ctypes.byref(att), int(rotary_dim), float(base),
+                                               ROTARY_SCALING[scaling], float(factor), int(original_context),
+                                               float(fast_turns), float(slow_turns))
     _check(st, "pkv_rotary_frequencies")
     return inv_freq, att.value
 
 
-def _inv_freq(t, D):
-    import torch
-    if t.dtype != torch.float32 or t.dim() != 1 or not 1 <= t.numel() <= D // 2:
+def _inv_freq(dev, t, D):
+    n = t.numel()
+    if t.dtype != _torch().float32 or t.dim() != 1 or not 1 <= n <= D // 2:
         raise TypeError("inv_freq must be float32 [rotary_dim / 2] with rotary_dim <= head_size")
-    return _contig(t, "inv_freq")
+    return _on(dev, t, "inv_freq"), 2 * n
+
+
+def _rotated_pair(dev, o, x, T, D, dtype, name):
+    """(out pointer, out stride, in pointer, in stride) of rows and their rotated rows."""
+    if o.shape != x.shape or o.dtype != dtype or x.dtype != dtype or x.shape[0] != T or x.shape[2] != D:
+        raise ValueError(f"{name} and {name}_out must be [T, heads, head_size] of q's dtype")
+    xp, xs = _rows(dev, x, name)
+    op, os = _rows(dev, o, name + "_out")
+    if op == xp and os != xs:
+        raise ValueError(f"{name}_out in place of {name} must have its strides")
+    return op, os, xp, xs
 
 
 def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, interleaved=False, attention_scale=1.0, stream=None):
     """Rotary positions of q [T, H, D] and k [T, Hkv, D] (rotary_embedding in
     pagedkv.h).  q_out / k_out may be q / k; k and k_out may be None.
     positions: int64 [T]; inv_freq: float32 [rotary_dim / 2] on the device."""
-    lib = load_library()
     T, H, D = q.shape
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    pairs = [(q_out, q, "q")] + ([] if k is None else [(k_out, k, "k")])
-    for o, x, name in pairs:
-        if o.shape != x.shape or o.dtype != q.dtype or x.dtype != q.dtype or x.shape[0] != T or x.shape[2] != D:
-            raise ValueError(f"{name} and {name}_out must be [T, heads, head_size] of q's dtype")
-        if o.data_ptr() == x.data_ptr() and T > 1 and o.stride(0) != x.stride(0):
-            raise ValueError(f"{name}_out in place of {name} must have its strides")
-        _same_device(q, o, x)
-    _same_device(q, positions, inv_freq)
-    qp, qs = _rows(q, "q")
-    qop, qos = _rows(q_out, "q_out")
-    kp, ks = (None, 0) if k is None else _rows(k, "k")
-    kop, kos = (None, 0) if k is None else _rows(k_out, "k_out")
-    st = lib.rotary_embedding(qop, kop, qp, kp, _int64(positions, T, "positions"), _inv_freq(inv_freq, D), T, H,
-                              0 if k is None else k.shape[1], D, 2 * inv_freq.numel(), int(bool(interleaved)),
-                              float(attention_scale), qos, kos, qs, ks, _dtype_code(q), _stream(stream, q.device))
-    _check(st, "rotary_embedding")
+    dev, dtype = _device(q, "q"), q.dtype
+    qop, qos, qp, qs = _rotated_pair(dev, q_out, q, T, D, dtype, "q")
+    kop, kos, kp, ks = (None, 0, None, 0) if k is None else _rotated_pair(dev, k_out, k, T, D, dtype, "k")
+    fp, rot = _inv_freq(dev, inv_freq, D)
+    _call("rotary_embedding", dev, stream, qop, kop, qp, kp, _int64(dev, positions, T, "positions"), fp, T, H,
+          0 if k is None else k.shape[1], D, rot, 1 if interleaved else 0, attention_scale, qos, kos, qs, ks,
+          _code(dtype))
 
 
-def _rotary_write(name, q_out, q, key, value, k_cache, v_cache, NB, Hkv, bs, positions, slot_mapping, inv_freq,
+def _rotary_write(name, caches, q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
                   interleaved, attention_scale, stream):
-    lib = load_library()
+    NB, Hkv, bs = caches
     T, H, D = q.shape
-    if q_out.shape != q.shape or tuple(key.shape) != (T, Hkv, D) or value.shape != key.shape:
-        raise ValueError("q, q_out, key and value must be [T, heads, head_size] and match the caches")
-    if q_out.dtype != q.dtype or key.dtype != q.dtype or value.dtype != q.dtype:
-        raise ValueError("q, q_out, key and value must share a dtype")
-    if q_out.data_ptr() == q.data_ptr() and T > 1 and q_out.stride(0) != q.stride(0):
-        raise ValueError("q_out in place of q must have its strides")
-    _same_device(q, q_out, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq)
-    qp, qs = _rows(q, "q")
-    qop, qos = _rows(q_out, "q_out")
-    kp, ks = _rows(key, "key")
-    vp, vs = _rows(value, "value")
-    st = getattr(lib, name)(qop, qp, kp, vp, _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
-                            _int64(positions, T, "positions"), _int64(slot_mapping, T, "slot_mapping"),
-                            _inv_freq(inv_freq, D), T, H, Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)),
-                            float(attention_scale), bs, NB, qos, qs, ks, vs, _dtype_code(q),
-                            _stream(stream, q.device))
-    _check(st, name)
+    dev, dtype = _device(q, "q"), q.dtype
+    if key.shape != (T, Hkv, D) or value.shape != key.shape or key.dtype != dtype or value.dtype != dtype:
+        raise ValueError("key and value must be [T, num_kv_heads, head_size] of q's dtype and match the caches")
+    qop, qos, qp, qs = _rotated_pair(dev, q_out, q, T, D, dtype, "q")
+    kp, ks = _rows(dev, key, "key")
+    vp, vs = _rows(dev, value, "value")
+    fp, rot = _inv_freq(dev, inv_freq, D)
+    _call(name, dev, stream, qop, qp, kp, vp, _on(dev, k_cache, "k_cache"), _on(dev, v_cache, "v_cache"),
+          _int64(dev, positions, T, "positions"), _int64(dev, slot_mapping, T, "slot_mapping"), fp, T, H, Hkv, D, rot,
+          1 if interleaved else 0, attention_scale, bs, NB, qos, qs, ks, vs, _code(dtype))
     return q_out
 
 
@@ -598,71 +644,58 @@ def rotary_reshape_and_cache(q_out, q, key, value, k_cache, v_cache, positions, 
                              interleaved=False, attention_scale=1.0, stream=None):
     """Rotary positions of q, and of key on its way into the cache with value
     (rotary_reshape_and_cache in pagedkv.h).  q_out may be q."""
-    NB, Hkv, bs, D = k_cache.shape
-    if D != q.shape[2] or v_cache.shape != k_cache.shape or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
-        raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size] of q's dtype")
-    return _rotary_write("rotary_reshape_and_cache", q_out, q, key, value, k_cache, v_cache, NB, Hkv, bs, positions,
-                         slot_mapping, inv_freq, interleaved, attention_scale, stream)
+    return _rotary_write("rotary_reshape_and_cache", _same_caches(k_cache, v_cache, q.shape[2], q.dtype), q_out, q,
+                         key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, interleaved,
+                         attention_scale, stream)
 
 
 def rotary_reshape_and_cache_fp8row(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
                                     interleaved=False, attention_scale=1.0, stream=None):
     """rotary_reshape_and_cache into 8-bit row caches
     (rotary_reshape_and_cache_fp8row in pagedkv.h)."""
-    NB, Hkv, bs = _row_caches(k_cache, v_cache, q.shape[2])
-    return _rotary_write("rotary_reshape_and_cache_fp8row", q_out, q, key, value, k_cache, v_cache, NB, Hkv, bs,
-                         positions, slot_mapping, inv_freq, interleaved, attention_scale, stream)
+    return _rotary_write("rotary_reshape_and_cache_fp8row", _row_caches(k_cache, v_cache, q.shape[2]), q_out, q, key,
+                         value, k_cache, v_cache, positions, slot_mapping, inv_freq, interleaved, attention_scale,
+                         stream)
 
 
 # ---------------------------------------------------------------------------
 # reading sequences back
 # ---------------------------------------------------------------------------
-def _gather(name, k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc, scales, stream):
-    import torch
-    lib = load_library()
+def _gather(name, caches, scales, k_out, v_out, k_cache, v_cache, block_tables, start_loc, stream):
+    int32 = _torch().int32
+    NB, Hkv, bs = caches
     T, Hkv2, D = k_out.shape
     if Hkv2 != Hkv or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
         raise ValueError("k_out and v_out must be [T, num_kv_heads, head_size] and match the caches")
-    if block_tables.dtype != torch.int32 or start_loc.dtype != torch.int32:
+    if block_tables.dtype != int32 or start_loc.dtype != int32:
         raise TypeError("block_tables and start_loc must be int32")
     S, MB = block_tables.shape
     if start_loc.numel() != S + 1:
         raise ValueError("start_loc must be [S + 1]")
-    _same_device(k_out, v_out, k_cache, v_cache, block_tables, start_loc)
-    st = getattr(lib, name)(_contig(k_out, "k_out"), _contig(v_out, "v_out"), _contig(k_cache, "k_cache"),
-                            _contig(v_cache, "v_cache"), _contig(block_tables, "block_tables"),
-                            _contig(start_loc, "start_loc"), *scales, T, S, Hkv, D, bs, NB, MB, _dtype_code(k_out),
-                            _stream(stream, k_out.device))
-    _check(st, name)
+    dev = _device(k_out, "k_out")
+    _call(name, dev, stream, _on(dev, k_out, "k_out"), _on(dev, v_out, "v_out"), _on(dev, k_cache, "k_cache"),
+          _on(dev, v_cache, "v_cache"), _on(dev, block_tables, "block_tables"), _on(dev, start_loc, "start_loc"),
+          *scales, T, S, Hkv, D, bs, NB, MB, _code(k_out.dtype))
     return k_out, v_out
 
 
 def gather_cache(k_out, v_out, k_cache, v_cache, block_tables, start_loc, stream=None):
     """Sequences read back from the pages (gather_cache in pagedkv.h): token t of
     sequence s goes to row start_loc[s] + t of k_out and v_out [T, Hkv, D]."""
-    NB, Hkv, bs, D = k_cache.shape
-    if D != k_out.shape[2] or v_cache.shape != k_cache.shape or k_cache.dtype != k_out.dtype \
-            or v_cache.dtype != k_out.dtype:
-        raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size] of k_out's dtype")
-    return _gather("gather_cache", k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc, (), stream)
+    return _gather("gather_cache", _same_caches(k_cache, v_cache, k_out.shape[2], k_out.dtype), (), k_out, v_out,
+                   k_cache, v_cache, block_tables, start_loc, stream)
 
 
 def gather_cache_fp8kv(k_out, v_out, k_cache, v_cache, block_tables, start_loc, k_scale, v_scale, stream=None):
     """gather_cache out of FP8 E4M3 caches with one scale for K and one for V."""
-    NB, Hkv, bs, D = k_cache.shape
-    if D != k_out.shape[2] or v_cache.shape != k_cache.shape:
-        raise ValueError("shape mismatch")
-    _fp8_cache(k_cache, "k_cache")
-    _fp8_cache(v_cache, "v_cache")
-    return _gather("gather_cache_fp8kv", k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc,
-                   (float(k_scale), float(v_scale)), stream)
+    return _gather("gather_cache_fp8kv", _e4m3_caches(k_cache, v_cache, k_out.shape[2]), (k_scale, v_scale), k_out,
+                   v_out, k_cache, v_cache, block_tables, start_loc, stream)
 
 
 def gather_cache_fp8row(k_out, v_out, k_cache, v_cache, block_tables, start_loc, stream=None):
     """gather_cache out of 8-bit row caches; k_out, v_out in f32/f16/bf16."""
-    NB, Hkv, bs = _row_caches(k_cache, v_cache, k_out.shape[2])
-    return _gather("gather_cache_fp8row", k_out, v_out, k_cache, v_cache, NB, Hkv, bs, block_tables, start_loc, (),
-                   stream)
+    return _gather("gather_cache_fp8row", _row_caches(k_cache, v_cache, k_out.shape[2]), (), k_out, v_out, k_cache,
+                   v_cache, block_tables, start_loc, stream)
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -116,8 +116,8 @@ struct PrefillShape {
     static constexpr uint32_t OFF_ITEMS = (OFF_BAR + 8 * NBAR + 63) / 64 * 64;   // item ring, 64 bytes a slot
     static constexpr uint32_t OFF_HOLD = OFF_ITEMS + 64 * IR;                   // tensor-memory address
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;  // 1 KB alignment slack
-    static constexpr int kSoftmaxRegs = 144, kSideRegs = 64;
-    static_assert(2 * kSoftmaxRegs + 3 * kSideRegs <= 5 * 96, "registers of the 640 threads at launch");
+    static constexpr int kSoftmaxRegs = 144, kIssueRegs = 64, kConvertRegs = 64;
+    static_assert(2 * kSoftmaxRegs + kIssueRegs + 2 * kConvertRegs <= 5 * 96, "registers of the 640 threads at launch");
     static constexpr uint32_t TM_TILE = 256;                // columns per query tile
     static constexpr uint32_t TM_S = 0;                     // S (N fp32 columns); P over its first N/2
     static constexpr uint32_t TM_O = N;                     // O at columns N .. N + D
@@ -130,7 +130,7 @@ struct PrefillShape {
 // An E4M3 cache takes two more warpgroups, whose warps convert the tiles (and
 // leaves the TMA warps 9 and 10 without work).  Its 640 threads start with 96
 // registers each, too few for the softmax's rows; the warpgroups share the
-// CTA's 5 * 96 a thread out again as 2 * kSoftmaxRegs + 3 * kSideRegs.
+// CTA's 5 * 96 a thread out again.
 template <typename T, typename TC>
 constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 640;
 
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     if (kConvert && warp >= 12) {
         // ===================== converting producers: warps 12-15 K, warps 16-19 V =====================
         if constexpr (kConvert) {
-            reg_dec<S::kSideRegs>();
+            reg_dec<S::kConvertRegs>();
             using Slice = SliceConverter<T, TC, D, BS>;
             constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
             static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
             __syncwarp();
         }
     } else if (warp >= 8) {
-        if constexpr (kConvert) reg_dec<S::kSideRegs>();
+        if constexpr (kConvert) reg_dec<S::kIssueRegs>();
         if (warp == 11) {
             // ===================== scheduler: items from the counter, q by TMA =====================
             const int pairs = p.num_seqs * Hkv;
