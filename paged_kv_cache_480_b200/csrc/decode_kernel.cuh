@@ -699,17 +699,20 @@ struct MmaConsumerFp8 {
         }
         n0 = fmaxf(m0, mx0);
         n1 = fmaxf(m1, mx1);
-        const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= al0;
-        l1 *= al1;
+        // past an item's first slices the maxima rarely move (factors of 1)
+        if (__any_sync(kFull, n0 != m0 || n1 != m1)) {
+            const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= al0;
+            l1 *= al1;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            o[m][0] *= al0;
-            o[m][2] *= al0;
-            o[m][1] *= al1;
-            o[m][3] *= al1;
+            for (int m = 0; m < MT; ++m) {
+                o[m][0] *= al0;
+                o[m][2] *= al0;
+                o[m][1] *= al1;
+                o[m][3] *= al1;
+            }
         }
     }
 
@@ -720,17 +723,21 @@ struct MmaConsumerFp8 {
         const int rows[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool ok = rows[i] < nvalid;       // masked tokens may hold NaN codes
             const unsigned char* vr = Vt + rows[i] * S::ROW + r * VB;
             if constexpr (VB == 16) {
-                uint4 v = *reinterpret_cast<const uint4*>(vr);
-                if (!ok) v = make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = *reinterpret_cast<const uint4*>(vr);
                 w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
             } else {
-                uint2 v = *reinterpret_cast<const uint2*>(vr);
-                if (!ok) v = make_uint2(0u, 0u);
+                const uint2 v = *reinterpret_cast<const uint2*>(vr);
                 w[i][0] = v.x; w[i][1] = v.y;
             }
+        }
+        if (nvalid < 16) {                          // masked tokens may hold NaN codes
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (rows[i] >= nvalid)
+#pragma unroll
+                    for (int k = 0; k < VB / 4; ++k) w[i][k] = 0u;
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
