@@ -946,6 +946,7 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
     unsigned char* nbuf = wb + L::nbuf(R);
     StageMeta* meta = reinterpret_cast<StageMeta*>(wb + L::meta(R));
     const uint32_t bar0 = smem_addr(wb + L::bars(R));
+    const uint32_t ring0 = smem_addr(ring);
     int PS = p.partition_size;
 
     if (lane == 0)
@@ -1044,7 +1045,62 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
     const TC* vc = reinterpret_cast<const TC*>(p.v_cache);
     const TQ* qg = reinterpret_cast<const TQ*>(p.q);
 
-    auto issue = [&]() {
+    // Over an FP8 cache blocks pass twice as fast, and what is done once a
+    // block outweighs its copies: a stage's record is one word, the item's
+    // output rows are written once, into the record of its q slot.
+    constexpr bool kLean = kIsFp8<TC>;
+    auto stage_word = [&](int st) -> int& { return meta[st].flags; };   // flags | nvalid << 8 | nh << 16 | qslot << 24
+    int lean_word = 0;    // the item's part of it
+    uint32_t lean_g = 0;  // its KV head
+    auto issue_lean = [&]() {
+        if (P.idx >= n_items) return;
+        const int st = issue_st;
+        const int phys = __shfl_sync(kFull, P.tbl, pj & 31);
+        int nvalid = min(max(P.ntok - pj * BS, 0), BS);
+        const bool bad = (unsigned)phys >= (unsigned)p.num_blocks && nvalid > 0;
+        if (bad) nvalid = 0;
+        if (pj == 0) {
+            int g = P.vg, sl = 0;
+            if (NSL > 1) {
+                g = P.vg / NSL;
+                sl = P.vg - g * NSL;
+            }
+            const int nh = min(G, Gr - sl * G);
+            lean_g = (uint32_t)g;
+            lean_word = (P.whole ? kWhole : 0) | (nh << 16) | (qslot_ctr << 24);
+            if (lane == 0) {
+                const int head0 = g * Gr + sl * G;
+                meta[qslot_ctr].pidx = (int64_t)P.jsp * p.num_heads + head0;
+                meta[qslot_ctr].obase = (int64_t)P.s * p.num_heads + head0;
+            }
+        }
+        if (lane == 0) {
+            stage_word(st) = lean_word | (pj == 0 ? kFirst : 0) | (pj == P.nblk - 1 ? kLast : 0) | (nvalid << 8);
+            const uint32_t bar = bar0 + 8 * st;
+            const uint32_t qbytes = pj == 0 ? (uint32_t)((lean_word >> 16) & 0xff) * S::QROW : 0u;
+            mbar_arrive_expect_tx(bar, qbytes + (nvalid > 0 ? 2 * S::TILE : 0));
+            if (pj == 0)
+                bulk_g2s(smem_addr(qbuf + qslot_ctr * S::QBYTES), qg + (size_t)meta[qslot_ctr].obase * D, qbytes, bar);
+            if (nvalid > 0) {
+                const uint64_t off = ((uint64_t)(uint32_t)phys * (uint32_t)Hkv + lean_g) * S::TILE;
+                const uint32_t dst = ring0 + (uint32_t)st * (2 * S::TILE);
+                bulk_g2s(dst, reinterpret_cast<const unsigned char*>(kc) + off, S::TILE, bar);
+                bulk_g2s(dst + S::TILE, reinterpret_cast<const unsigned char*>(vc) + off, S::TILE, bar);
+            }
+            if (bad) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+        }
+        ++issued;
+        issue_st = (st + 1 == R) ? 0 : st + 1;
+        if (++pj == P.nblk) {
+            P = PN;
+            pj = 0;
+            qslot_ctr = (qslot_ctr + 1 == R) ? 0 : qslot_ctr + 1;
+            PN = fetch(raw_next);
+            raw_next = (PN.idx < n_items) ? next_index() : n_items;
+        }
+    };
+
+    auto issue_full = [&]() {
         if (P.idx >= n_items) return;
         const int st = issue_st;
         if constexpr (kLongItems) {
@@ -1118,6 +1174,11 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
         }
     };
 
+    auto issue = [&]() {
+        if constexpr (kLean) issue_lean();
+        else issue_full();
+    };
+
     // ---- consumer ----
     ConsumerFor<TQ, TC, D, BS, G> cons;
     const float qscale = p.scale_log2 * p.k_scale;   // logits in log2 units, cache scale folded in
@@ -1141,21 +1202,32 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
             lost = true;
             break;
         }
-        // Over an FP8 cache (threads capped at 128 registers) only what the block
-        // needs is held in registers and finish() reads the item's output rows
-        // from the stage's metadata; the 16-bit kernels keep a copy (measured:
-        // each way is the faster one for its kernel).
-        constexpr bool kLean = kIsFp8<TC>;
+        // (the 16-bit kernels keep a copy of the stage's record in registers;
+        // measured: each way is the faster one for its kernel)
         StageMeta mt;
         if constexpr (kLean) {
-            mt.flags = meta[cons_st].flags;
-            mt.nvalid = meta[cons_st].nvalid;
-            mt.newrow = meta[cons_st].newrow;
+            const int w = stage_word(cons_st);
+            mt.flags = w & 0xff;
+            mt.nvalid = (w >> 8) & 0xff;
+            mt.nh = (w >> 16) & 0xff;
+            mt.qslot = (w >> 24) & 0xff;
+            mt.newrow = -1;
         } else {
             mt = meta[cons_st];
         }
+        // what finish() reads of an item
+        auto finish = [&](const StageMeta& m) {
+            if constexpr (kLean) {
+                StageMeta f = m;
+                f.pidx = meta[m.qslot].pidx;
+                f.obase = meta[m.qslot].obase;
+                cons.finish(f, p);
+            } else {
+                cons.finish(m, p);
+            }
+        };
         // (a column count of 1 or 2 only ever holds a whole group of that size)
-        if (mt.flags & kFirst) cons.begin(qbuf + meta[cons_st].qslot * S::QBYTES, qscale, G <= 2 ? G : meta[cons_st].nh);
+        if (mt.flags & kFirst) cons.begin(qbuf + mt.qslot * S::QBYTES, qscale, G <= 2 ? G : mt.nh);
         using Cons = ConsumerFor<TQ, TC, D, BS, G>;
         if constexpr (Cons::kPairs) {
             // the item's next block is in the next stage: take both together
@@ -1167,12 +1239,13 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
                     lost = true;
                     break;
                 }
-                const int nvalid2 = meta[st2].nvalid;
-                if (nvalid2 > 0 && meta[st2].newrow < 0) {
+                const int w2 = stage_word(st2);      // (only FP8 kernels take pairs)
+                const int nvalid2 = (w2 >> 8) & 0xff;
+                if (nvalid2 > 0) {
                     const unsigned char* Ka = ring + (size_t)cons_st * 2 * S::TILE;
                     const unsigned char* Kb = ring + (size_t)st2 * 2 * S::TILE;
                     cons.block2(Ka, Ka + S::TILE, mt.nvalid, Kb, Kb + S::TILE, nvalid2, qscale);
-                    if (meta[st2].flags & kLast) cons.finish(meta[st2], p);
+                    if (w2 & kLast) finish(mt);      // (one item: the same rows)
                     __syncwarp();
                     consumed += 2;
                     cons_st = st2;
@@ -1209,10 +1282,7 @@ __global__ void __launch_bounds__(decode_max_threads<TQ, TC, G>(), 1) paged_deco
             const unsigned char* Kt = ring + (size_t)cons_st * 2 * S::TILE;
             cons.block(Kt, Kt + S::TILE, mt.nvalid, qscale);
         }
-        if (mt.flags & kLast) {
-            if constexpr (kLean) cons.finish(meta[cons_st], p);
-            else cons.finish(mt, p);
-        }
+        if (mt.flags & kLast) finish(mt);
         __syncwarp();
         ++consumed;
         if (++cons_st == R) { cons_st = 0; phase ^= 1u; }
