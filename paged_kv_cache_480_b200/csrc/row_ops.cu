@@ -2,6 +2,8 @@
 // fused with the cache write), the quantising cache write, and the read-back
 // of whole sequences.  All are bound by HBM (each element is read and written
 // once) for many tokens and by latency for a few.
+#include <climits>
+
 #include "common.cuh"
 #include "fp8row.cuh"
 #include "pagedkv.h"
@@ -10,7 +12,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Row lengths are multiples of 2 * kPerChunk elements, and a thread takes
 // kPerChunk pairs of one row: rotary pairs (2i, 2i + 1) or (i, i + rot / 2),
@@ -34,22 +36,32 @@ struct Unit {
         return make_int2(2 * i, 2 * i + 1);
     }
 
-    // x[j], x[E + j]: the unit's j-th pair if `halves`, else x in memory order
-    __device__ __forceinline__ static void load(const T* row, int u, int rot, float (&x)[2 * E]) {
+    // A unit's elements as they are in memory: its two chunks, or (not VEC) its
+    // first and its second elements packed into two chunks.
+    struct Raw {
+        uint4 a, b;
+    };
+    __device__ __forceinline__ static Raw fetch(const T* row, int u, int rot) {
+        Raw x;
         if constexpr (VEC) {
             const int2 c = chunks(u, rot);
-            const uint4 a = *reinterpret_cast<const uint4*>(row + c.x);
-            const uint4 b = *reinterpret_cast<const uint4*>(row + c.y);
-            Elem<T>::widen(a, x);
-            Elem<T>::widen(b, x + E);
+            x.a = *reinterpret_cast<const uint4*>(row + c.x);
+            x.b = *reinterpret_cast<const uint4*>(row + c.y);
         } else {
+            T* a = reinterpret_cast<T*>(&x.a);
+            T* b = reinterpret_cast<T*>(&x.b);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 const int2 c = pair(u * E + j, rot);
-                x[j] = (float)row[c.x];
-                x[E + j] = (float)row[c.y];
+                a[j] = row[c.x];
+                b[j] = row[c.y];
             }
         }
+        return x;
+    }
+    __device__ __forceinline__ static void widen(const Raw& r, float (&x)[2 * E]) {
+        Elem<T>::widen(r.a, x);
+        Elem<T>::widen(r.b, x + E);
     }
 
     __device__ __forceinline__ static void rotate(const float2* cs, int u, int rot, float (&x)[2 * E]) {
@@ -128,103 +140,138 @@ __device__ __forceinline__ float2 turn(int64_t position, float inv_freq, float m
 }
 
 // grid.x takes tokens (tokens_cta a CTA), grid.y parts of a token's units (a
-// few tokens are spread over the SMs that way).  The CTA first takes cos and
-// sin of its tokens' positions, one thread a frequency, into shared memory
-// where every head of the token reads them: with up to a hundred rows a token
-// the angles cost a few percent of the row work.
+// few tokens are spread over the SMs that way).  A thread takes kDepth units
+// at a time and has all their loads in flight before it works on the first;
+// those of the first round are requested before the CTA takes cos and sin of
+// its tokens' positions, one thread a frequency, into shared memory where every
+// head of the token reads them.
+constexpr int kDepth = 2;
+constexpr int kMaxTokens = 8;   // of a CTA
+
 template <typename T, RowSink SINK, bool INTERLEAVED, bool VEC>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kThreads + 32) rotary_kernel(const RotaryParams p) {
     using U = Unit<T, INTERLEAVED, VEC>;
     using UV = Unit<T, true, true>;        // rows that are not rotated: plain chunks
     constexpr int E = U::E;
+    constexpr bool kCached = SINK != RowSink::kRows;
     extern __shared__ float2 cs_all[];
+    __shared__ int64_t slots[kMaxTokens];
     griddep_wait();
     griddep_launch();
     const int half = p.rot / 2;
     const int64_t token0 = (int64_t)blockIdx.x * p.tokens_cta;
     const int tokens = (int)min((int64_t)p.tokens_cta, p.num_tokens - token0);
-    for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
-        const int t = i / half;
-        cs_all[i] = turn(p.positions[token0 + t], p.inv_freq[i - t * half], p.mscale);
-    }
-    __syncthreads();
-
     const int first = blockIdx.y * p.units_cta;
     const int last = min(first + p.units_cta, p.units_token * tokens);
-    const int D = p.head_size;
-    // whole warps stay in the loop: quantised rows shuffle over their lanes
-    for (int base = first + (threadIdx.x & ~31); base < last; base += blockDim.x) {
-        const int w = base + (threadIdx.x & 31);
-        const bool on = w < last;
-        const int t = on ? w / p.units_token : 0;
-        const int rem = on ? w - t * p.units_token : 0;
-        const int row = rem / p.units_row, u = rem - row * p.units_row;
-        const int64_t token = token0 + t;
-        const float2* cs = cs_all + t * half;
-        float x[2 * E];
-        if (row < p.num_heads) {
-            if (on) {
-                U::load(static_cast<const T*>(p.q) + token * p.q_stride + (int64_t)row * D, u, p.rot, x);
-                U::rotate(cs, u, p.rot, x);
-                U::store(static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)row * D, u, p.rot, x);
-            }
-            if constexpr (SINK != RowSink::kCacheFp8Row) continue;
+    const int D = p.head_size, H = p.num_heads, Hkv = p.num_kv_heads;
+
+    // Unit w of the CTA: token t, row (q rows, then k, then v), part u of the row.
+    struct Where {
+        int t, row, u;
+    };
+    auto where = [&](int w) {
+        Where x{-1, 0, 0};
+        if (w < last) {
+            x.t = tokens == 1 ? 0 : w / p.units_token;
+            const int rem = w - x.t * p.units_token;
+            x.row = rem / p.units_row;
+            x.u = rem - x.row * p.units_row;
         }
-        if constexpr (SINK == RowSink::kRows) {
-            const int g = row - p.num_heads;
-            if (on) {
-                U::load(static_cast<const T*>(p.k) + token * p.k_stride + (int64_t)g * D, u, p.rot, x);
-                U::rotate(cs, u, p.rot, x);
-                U::store(static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)g * D, u, p.rot, x);
+        return x;
+    };
+    auto fetch = [&](const Where& x) {
+        typename U::Raw r;
+        r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
+        if (x.t >= 0) {
+            const int64_t token = token0 + x.t;
+            if (x.row < H) {
+                r = U::fetch(static_cast<const T*>(p.q) + token * p.q_stride + (int64_t)x.row * D, x.u, p.rot);
+            } else if (!kCached || x.row < H + Hkv) {
+                r = U::fetch(static_cast<const T*>(p.k) + token * p.k_stride + (int64_t)(x.row - H) * D, x.u, p.rot);
+            } else {
+                const typename UV::Raw v =
+                    UV::fetch(static_cast<const T*>(p.v) + token * p.v_stride + (int64_t)(x.row - H - Hkv) * D, x.u, 0);
+                r.a = v.a;
+                r.b = v.b;
             }
+        }
+        return r;
+    };
+    auto finish = [&](const Where& w, const typename U::Raw& raw) {
+        float x[2 * E];
+        U::widen(raw, x);
+        const bool is_v = kCached && w.row >= H + Hkv;
+        const int64_t token = token0 + w.t;
+        if (w.t >= 0 && !is_v) U::rotate(cs_all + w.t * half, w.u, p.rot, x);
+        if (w.t >= 0 && w.row < H)
+            U::store(static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)w.row * D, w.u, p.rot, x);
+        if constexpr (!kCached) {
+            if (w.t >= 0 && w.row >= H)
+                U::store(static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)(w.row - H) * D, w.u, p.rot, x);
         } else {
-            const bool kv = on && row >= p.num_heads;
-            const bool is_v = row >= p.num_heads + p.num_kv_heads;
-            const int g = row - p.num_heads - (is_v ? p.num_kv_heads : 0);
+            const int g = w.row - H - (is_v ? Hkv : 0);
             int64_t slot = -1;
-            if (kv) {
-                slot = p.slot_mapping[token];
+            if (w.t >= 0 && w.row >= H) {
+                slot = slots[w.t];
                 if (slot >= p.pool_slots) {
-                    if (u == 0 && g == 0 && !is_v) flag_error(p.errors, PKV_DEVERR_SLOT);
+                    if (w.u == 0 && g == 0 && !is_v) flag_error(p.errors, PKV_DEVERR_SLOT);
                     slot = -1;
                 }
             }
             const bool put = slot >= 0;
-            if (put) {
-                if (is_v) {
-                    UV::load(static_cast<const T*>(p.v) + token * p.v_stride + (int64_t)g * D, u, 0, x);
-                } else {
-                    U::load(static_cast<const T*>(p.k) + token * p.k_stride + (int64_t)g * D, u, p.rot, x);
-                    U::rotate(cs, u, p.rot, x);
-                }
-            }
             const int64_t blk = slot >> p.block_shift;
             const int bs = 1 << p.block_shift;
             const int off = (int)(slot & (bs - 1));
             unsigned char* cache = is_v ? p.v_cache : p.k_cache;
             if constexpr (SINK == RowSink::kCache) {
                 if (put) {
-                    T* dst = reinterpret_cast<T*>(cache) + ((blk * p.num_kv_heads + g) * bs + off) * D;
-                    if (is_v) UV::store(dst, u, 0, x);
-                    else U::store(dst, u, p.rot, x);
+                    T* dst = reinterpret_cast<T*>(cache) + ((blk * Hkv + g) * bs + off) * D;
+                    if (is_v) UV::store(dst, w.u, 0, x);
+                    else U::store(dst, w.u, p.rot, x);
                 }
-            } else {
+            } else if (__any_sync(0xffffffffu, put)) {
                 // the row's largest magnitude over its D / (2 E) lanes
                 uint32_t top = 0;
-                if (put) {
 #pragma unroll
-                    for (int j = 0; j < 2 * E; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-                }
+                for (int j = 0; j < 2 * E; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
                 for (int o = 1; o < p.units_row; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                 if (put) {
                     const int b = row_scale_byte(top);
-                    unsigned char* tile = cache + (blk * p.num_kv_heads + g) * (int64_t)(bs * (D + 1));
-                    if (is_v) UV::store_codes(tile + off * D, u, 0, x, row_scale_inv(b));
-                    else U::store_codes(tile + off * D, u, p.rot, x, row_scale_inv(b));
-                    if (u == 0) tile[bs * D + off] = (unsigned char)b;
+                    unsigned char* tile = cache + (blk * Hkv + g) * (int64_t)(bs * (D + 1));
+                    if (is_v) UV::store_codes(tile + off * D, w.u, 0, x, row_scale_inv(b));
+                    else U::store_codes(tile + off * D, w.u, p.rot, x, row_scale_inv(b));
+                    if (w.u == 0) tile[bs * D + off] = (unsigned char)b;
                 }
             }
         }
+    };
+
+    // (whole warps stay in the loop: quantised rows shuffle over their lanes)
+    const int step = blockDim.x * kDepth;
+    Where at[kDepth];
+    typename U::Raw raw[kDepth];
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) {
+        at[k] = where(first + k * (int)blockDim.x + (int)threadIdx.x);
+        raw[k] = fetch(at[k]);
+    }
+    if constexpr (kCached)
+        if ((int)threadIdx.x < tokens) slots[threadIdx.x] = p.slot_mapping[token0 + threadIdx.x];
+    for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+        const int t = i / half;
+        cs_all[i] = turn(p.positions[token0 + t], p.inv_freq[i - t * half], p.mscale);
+    }
+    __syncthreads();
+    for (int base = first; base < last; base += step) {
+        if (base != first) {
+#pragma unroll
+            for (int k = 0; k < kDepth; ++k) {
+                at[k] = where(base + k * (int)blockDim.x + (int)threadIdx.x);
+                raw[k] = fetch(at[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) finish(at[k], raw[k]);
     }
 }
 
@@ -235,26 +282,36 @@ cudaError_t run_rotary(RotaryParams& p, bool interleaved, int num_sms, cudaStrea
     const int rows = p.num_heads + p.num_kv_heads * (SINK == RowSink::kRows ? 1 : 2);
     p.units_token = rows * p.units_row;
     if (p.num_tokens == 0 || p.units_token == 0) return cudaSuccess;
-    // A CTA takes whole tokens, enough of them for two units a thread (at most
-    // 8 tokens: their angles stay within 16 KB); with too few such CTAs for the
+    // A CTA takes whole tokens, enough of them for kDepth units a thread (at most
+    // kMaxTokens: their angles stay within 16 KB); with too few such CTAs for the
     // SMs a token's units are split into parts of one unit a thread.
-    const int want = 2 * kThreads;
-    int tpc = want / p.units_token;
-    tpc = tpc < 1 ? 1 : tpc > 8 ? 8 : tpc;
+    constexpr int kRound = kDepth * kThreads;
+    int tpc = kRound / p.units_token;
+    tpc = tpc < 1 ? 1 : tpc > kMaxTokens ? kMaxTokens : tpc;
     while (tpc > 1 && (p.num_tokens + tpc - 1) / tpc < 4 * num_sms) tpc >>= 1;
     const int groups = (p.num_tokens + tpc - 1) / tpc;
     p.tokens_cta = tpc;
     p.units_cta = p.units_token * tpc;
-    int parts = 1;
+    int parts = 1, depth = kDepth;
     if (tpc == 1 && groups < 4 * num_sms) {
         const int most = (p.units_token + kThreads - 1) / kThreads;
         parts = (4 * num_sms + groups - 1) / groups;
         if (parts > most) parts = most;
         p.units_cta = ((p.units_token + parts - 1) / parts + 31) / 32 * 32;
         parts = (p.units_token + p.units_cta - 1) / p.units_cta;
+        depth = 1;
     }
-    int threads = (p.units_cta + 31) / 32 * 32;
-    if (threads > kThreads) threads = kThreads;
+    // about 128 threads (measured on packed prompts and on chunks: 256 are 5-10%
+    // slower), the count that leaves the fewest without a unit in the last round
+    int threads = kThreads, idle = INT_MAX;
+    for (int t = kThreads + 32; t >= kThreads - 32; t -= 32) {
+        const int round = t * depth, over = (p.units_cta + round - 1) / round * round - p.units_cta;
+        if (over < idle || (over == idle && t == kThreads)) {
+            threads = t;
+            idle = over;
+        }
+    }
+    if (p.units_cta < threads) threads = (p.units_cta + 31) / 32 * 32;
     const size_t smem = sizeof(float2) * (size_t)tpc * (p.rot / 2);
     const dim3 grid((unsigned)groups, (unsigned)parts), block((unsigned)threads);
     if (interleaved) return launch_pdl(rotary_kernel<T, SINK, true, true>, grid, block, smem, stream, p);
@@ -277,10 +334,10 @@ cudaError_t by_sink(RotaryParams& p, RowSink sink, bool interleaved, int num_sms
 // one that starts at or before it) and block once, then the threads copy or
 // convert 16 cache bytes each, K and V.
 // ---------------------------------------------------------------------------
-constexpr int kGatherTokens = 32;
+constexpr int kGatherTokens = 32, kGatherThreads = 128;
 
 template <typename T, CacheKind KIND>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
     constexpr int ES = KIND == CacheKind::kSame ? (int)sizeof(T) : 1;   // bytes of a cache element
     constexpr int EPU = 16 / ES;                                        // elements of a unit
     __shared__ int s_phys[kGatherTokens];   // physical block; -1: zeros (a bad id); -2: no row
@@ -350,12 +407,12 @@ cudaError_t run_gather(GatherParams& p, int num_sms, cudaStream_t stream) {
     if (p.num_tokens == 0) return cudaSuccess;
     // enough tokens for eight units a thread, fewer while the SMs are not filled
     const int per_token = 2 * p.num_kv_heads * p.head_size / (KIND == CacheKind::kSame ? 16 / (int)sizeof(T) : 16);
-    int tpc = 8 * kThreads / per_token;
+    int tpc = 8 * kGatherThreads / per_token;
     tpc = tpc < 1 ? 1 : tpc > kGatherTokens ? kGatherTokens : tpc;
     while (tpc > 1 && (p.num_tokens + tpc - 1) / tpc < 4 * num_sms) tpc >>= 1;
     p.tokens_cta = tpc;
     const dim3 grid((unsigned)((p.num_tokens + tpc - 1) / tpc));
-    return launch_pdl(gather_kernel<T, KIND>, grid, dim3(kThreads), 0, stream, p);
+    return launch_pdl(gather_kernel<T, KIND>, grid, dim3(kGatherThreads), 0, stream, p);
 }
 
 template <typename T>
