@@ -12,7 +12,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;        // about that many a CTA; twice that when a token is split
+constexpr int kMostThreads = 160;
 
 // Row lengths are multiples of 2 * kPerChunk elements, and a thread takes
 // kPerChunk pairs of one row: rotary pairs (2i, 2i + 1) or (i, i + rot / 2),
@@ -64,14 +65,19 @@ struct Unit {
         Elem<T>::widen(r.b, x + E);
     }
 
-    __device__ __forceinline__ static void rotate(const float2* cs, int u, int rot, float (&x)[2 * E]) {
+    // Where a token's pair i keeps its cos and sin: the pairs of one unit lie
+    // `span` = ceil(rot / 2 / E) apart, so that neighbouring units read
+    // neighbouring words (together, a unit's pairs would put four lanes of
+    // every read on one bank).
+    __device__ __forceinline__ static int angle(int i, int span) { return i % E * span + i / E; }
+
+    __device__ __forceinline__ static void rotate(const float2* cs, int span, int u, int rot, float (&x)[2 * E]) {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const int i = u * E + j;
             float& a = x[INTERLEAVED ? 2 * j : j];
             float& b = x[INTERLEAVED ? 2 * j + 1 : E + j];
-            if (i < rot / 2) {
-                const float2 w = cs[i];
+            if (u * E + j < rot / 2) {
+                const float2 w = cs[j * span + u];
                 const float y = a * w.x - b * w.y;
                 b = b * w.x + a * w.y;
                 a = y;
@@ -128,6 +134,12 @@ struct Unit {
     }
 };
 
+// n / d for small numbers (n * d below 2^32), from the launcher's inverse of d.
+__device__ __forceinline__ int divide(int n, uint32_t inverse) {
+    return inverse ? (int)__umulhi((uint32_t)n, inverse) : n;
+}
+uint32_t inverse_of(int d) { return d == 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + d - 1) / d); }
+
 // cos and sin of position * inv_freq.  The product and its reduction to a
 // fraction of a turn are in fp64 (an fp32 angle of a far position is off by
 // whole radians); the fraction, below half a turn, is exact enough in fp32.
@@ -149,7 +161,7 @@ constexpr int kDepth = 2;
 constexpr int kMaxTokens = 8;   // of a CTA
 
 template <typename T, RowSink SINK, bool INTERLEAVED, bool VEC>
-__global__ void __launch_bounds__(kThreads + 32) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kMostThreads) rotary_kernel(const RotaryParams p) {
     using U = Unit<T, INTERLEAVED, VEC>;
     using UV = Unit<T, true, true>;        // rows that are not rotated: plain chunks
     constexpr int E = U::E;
@@ -158,7 +170,7 @@ __global__ void __launch_bounds__(kThreads + 32) rotary_kernel(const RotaryParam
     __shared__ int64_t slots[kMaxTokens];
     griddep_wait();
     griddep_launch();
-    const int half = p.rot / 2;
+    const int half = p.rot / 2, span = (half + E - 1) / E;
     const int64_t token0 = (int64_t)blockIdx.x * p.tokens_cta;
     const int tokens = (int)min((int64_t)p.tokens_cta, p.num_tokens - token0);
     const int first = blockIdx.y * p.units_cta;
@@ -172,9 +184,9 @@ __global__ void __launch_bounds__(kThreads + 32) rotary_kernel(const RotaryParam
     auto where = [&](int w) {
         Where x{-1, 0, 0};
         if (w < last) {
-            x.t = tokens == 1 ? 0 : w / p.units_token;
+            x.t = tokens == 1 ? 0 : divide(w, p.token_inverse);
             const int rem = w - x.t * p.units_token;
-            x.row = rem / p.units_row;
+            x.row = divide(rem, p.row_inverse);
             x.u = rem - x.row * p.units_row;
         }
         return x;
@@ -202,7 +214,7 @@ __global__ void __launch_bounds__(kThreads + 32) rotary_kernel(const RotaryParam
         U::widen(raw, x);
         const bool is_v = kCached && w.row >= H + Hkv;
         const int64_t token = token0 + w.t;
-        if (w.t >= 0 && !is_v) U::rotate(cs_all + w.t * half, w.u, p.rot, x);
+        if (w.t >= 0 && !is_v) U::rotate(cs_all + w.t * (span * E), span, w.u, p.rot, x);
         if (w.t >= 0 && w.row < H)
             U::store(static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)w.row * D, w.u, p.rot, x);
         if constexpr (!kCached) {
@@ -259,7 +271,8 @@ __global__ void __launch_bounds__(kThreads + 32) rotary_kernel(const RotaryParam
         if ((int)threadIdx.x < tokens) slots[threadIdx.x] = p.slot_mapping[token0 + threadIdx.x];
     for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
         const int t = i / half;
-        cs_all[i] = turn(p.positions[token0 + t], p.inv_freq[i - t * half], p.mscale);
+        const int k = i - t * half;
+        cs_all[t * (span * E) + U::angle(k, span)] = turn(p.positions[token0 + t], p.inv_freq[k], p.mscale);
     }
     __syncthreads();
     for (int base = first; base < last; base += step) {
@@ -292,27 +305,31 @@ cudaError_t run_rotary(RotaryParams& p, bool interleaved, int num_sms, cudaStrea
     const int groups = (p.num_tokens + tpc - 1) / tpc;
     p.tokens_cta = tpc;
     p.units_cta = p.units_token * tpc;
-    int parts = 1, depth = kDepth;
+    int parts = 1, depth = kDepth, about = kThreads;
     if (tpc == 1 && groups < 4 * num_sms) {
-        const int most = (p.units_token + kThreads - 1) / kThreads;
+        about = 2 * kThreads;
+        const int most = (p.units_token + about - 1) / about;
         parts = (4 * num_sms + groups - 1) / groups;
         if (parts > most) parts = most;
         p.units_cta = ((p.units_token + parts - 1) / parts + 31) / 32 * 32;
         parts = (p.units_token + p.units_cta - 1) / p.units_cta;
         depth = 1;
     }
-    // about 128 threads (measured on packed prompts and on chunks: 256 are 5-10%
-    // slower), the count that leaves the fewest without a unit in the last round
-    int threads = kThreads, idle = INT_MAX;
-    for (int t = kThreads + 32; t >= kThreads - 32; t -= 32) {
+    // about 64 threads (chunks with the quantising write, 8192 tokens of 64 + 8
+    // heads: 63.9 us; 67.2 with 128 and 72 with 256), the count that leaves the
+    // fewest without a unit in the last round
+    int threads = about, idle = INT_MAX;
+    for (int t = about + 32; t >= about - 32; t -= 32) {
         const int round = t * depth, over = (p.units_cta + round - 1) / round * round - p.units_cta;
-        if (over < idle || (over == idle && t == kThreads)) {
+        if (over < idle || (over == idle && t == about)) {
             threads = t;
             idle = over;
         }
     }
     if (p.units_cta < threads) threads = (p.units_cta + 31) / 32 * 32;
-    const size_t smem = sizeof(float2) * (size_t)tpc * (p.rot / 2);
+    p.row_inverse = inverse_of(p.units_row);
+    p.token_inverse = inverse_of(p.units_token);
+    const size_t smem = sizeof(float2) * (size_t)tpc * ((p.rot / 2 + E - 1) / E * E);
     const dim3 grid((unsigned)groups, (unsigned)parts), block((unsigned)threads);
     if (interleaved) return launch_pdl(rotary_kernel<T, SINK, true, true>, grid, block, smem, stream, p);
     if ((p.rot / 2) % E == 0) return launch_pdl(rotary_kernel<T, SINK, false, true>, grid, block, smem, stream, p);

@@ -31,6 +31,7 @@ struct RotaryParams {
     int units_row;             // threads a row takes
     int units_token;           // threads a token takes
     int tokens_cta, units_cta; // tokens a CTA takes; units of its tokens it takes (grid.y parts)
+    uint32_t row_inverse, token_inverse;   // divide by units_row and units_token
 };
 
 cudaError_t launch_rotary(RotaryParams p, RowSink sink, bool interleaved, int dtype, int num_sms, cudaStream_t stream);
