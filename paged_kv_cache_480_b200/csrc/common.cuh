@@ -224,6 +224,11 @@ __device__ __forceinline__ void flag_error(unsigned int* flags, unsigned int bit
     if (flags) atomicOr(flags, bit);
 }
 
+// Registers a thread of the executing warpgroup, whose warps all take the same
+// call: dec gives some back to the CTA's pool, inc waits until they are there.
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialisation: it may become resident while its
 // predecessor on the stream finishes, and waits (griddep_wait) for that

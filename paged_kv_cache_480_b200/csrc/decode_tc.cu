@@ -11,9 +11,9 @@
 namespace pkv {
 namespace {
 
-template <typename T, int D, int BS>
+template <typename T, typename TC, int D, int BS>
 pkv_status run(const DecodeTcArgs& a, cudaStream_t stream) {
-    using S = DecodeTcShape<T, D, BS>;
+    using S = DecodeTcShape<T, TC, D, BS>;
     const CUtensorMapDataType type =
         std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t esz = sizeof(T);
@@ -27,8 +27,10 @@ pkv_status run(const DecodeTcArgs& a, cudaStream_t stream) {
         if (!encode_tiled(&tm_q, type, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return PKV_ERR_CUDA;
     }
     const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * BS;
-    if (rows > 0x7fffffff - BS) return PKV_ERR_UNSUPPORTED;
-    {
+    if (!S::kConvert && rows > 0x7fffffff - BS) return PKV_ERR_UNSUPPORTED;   // (a tensor map's row index)
+    if constexpr (S::kConvert) {
+        tm_k = tm_v = tm_q;                  // not read
+    } else {
         const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
         const cuuint64_t strides[1] = {D * esz};
         const cuuint32_t box[2] = {64, (cuuint32_t)BS};
@@ -55,8 +57,10 @@ pkv_status run(const DecodeTcArgs& a, cudaStream_t stream) {
     p.slices = (G + S::M - 1) / S::M;
     p.rows = GR;
     p.cache_rows = (int)rows;
+    p.k_cache = static_cast<const unsigned char*>(a.k_cache);
+    p.v_cache = static_cast<const unsigned char*>(a.v_cache);
     p.wait_limit = a.wait_limit;
-    auto kernel = paged_decode_tc_kernel<T, D, BS>;
+    auto kernel = paged_decode_tc_kernel<T, TC, D, BS>;
     static std::atomic<bool> configured[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PKV_ERR_CUDA;
@@ -66,7 +70,7 @@ pkv_status run(const DecodeTcArgs& a, cudaStream_t stream) {
             return PKV_ERR_CUDA;
         configured[dev].store(true, std::memory_order_release);
     }
-    if (launch_pdl(kernel, dim3(kDecodeTcCtas), dim3(kDecodeTcThreads), S::SMEM, stream, p, tm_q, tm_k, tm_v) !=
+    if (launch_pdl(kernel, dim3(kDecodeTcCtas), dim3(kDecodeTcThreads<T, TC>), S::SMEM, stream, p, tm_q, tm_k, tm_v) !=
         cudaSuccess)
         return PKV_ERR_CUDA;
 
@@ -87,22 +91,27 @@ pkv_status run(const DecodeTcArgs& a, cudaStream_t stream) {
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <typename T, int D>
+template <typename T, typename TC, int D>
 pkv_status by_block(const DecodeTcArgs& a, cudaStream_t stream) {
     switch (a.block_size) {
-        case 16: return run<T, D, 16>(a, stream);
-        case 32: return run<T, D, 32>(a, stream);
+        case 16: return run<T, TC, D, 16>(a, stream);
+        case 32: return run<T, TC, D, 32>(a, stream);
+        default: return PKV_ERR_UNSUPPORTED;
+    }
+}
+
+template <typename T, typename TC>
+pkv_status by_head(const DecodeTcArgs& a, cudaStream_t stream) {
+    switch (a.head_size) {
+        case 64: return by_block<T, TC, 64>(a, stream);
+        case 128: return by_block<T, TC, 128>(a, stream);
         default: return PKV_ERR_UNSUPPORTED;
     }
 }
 
 template <typename T>
-pkv_status by_head(const DecodeTcArgs& a, cudaStream_t stream) {
-    switch (a.head_size) {
-        case 64: return by_block<T, 64>(a, stream);
-        case 128: return by_block<T, 128>(a, stream);
-        default: return PKV_ERR_UNSUPPORTED;
-    }
+pkv_status by_kind(const DecodeTcArgs& a, cudaStream_t stream) {
+    return a.kind == CacheKind::kFp8Row ? by_head<T, fp8row>(a, stream) : by_head<T, T>(a, stream);
 }
 
 }  // namespace
@@ -115,8 +124,8 @@ size_t decode_tc_partial_rows(int num_seqs, int num_heads, int num_kv_heads) {
 
 pkv_status launch_decode_tc(const DecodeTcArgs& a, cudaStream_t stream) {
     switch (a.dtype) {
-        case PKV_F16: return by_head<__half>(a, stream);
-        case PKV_BF16: return by_head<__nv_bfloat16>(a, stream);
+        case PKV_F16: return by_kind<__half>(a, stream);
+        case PKV_BF16: return by_kind<__nv_bfloat16>(a, stream);
         default: return PKV_ERR_UNSUPPORTED;
     }
 }

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "pagedkv.h"
+#include "row_ops.cuh"
 
 namespace pkv {
 
@@ -31,6 +32,7 @@ struct DecodeTcArgs {
     int num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks;
     int max_blocks_per_seq, max_context_len;
     pkv_dtype dtype;
+    CacheKind kind;      // kSame or kFp8Row
     uint32_t wait_limit;
 };
 

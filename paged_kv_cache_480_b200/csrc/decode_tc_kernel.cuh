@@ -31,7 +31,10 @@
 //   warps 0-3, 4-7  softmax and partial write of half 0 and 1, one row per thread;
 //   warp 8          issues the MMAs (one thread);
 //   warp 9          streams q and K by TMA;  warp 10  streams V by TMA and
-//                   zeroes the V rows past a context's end in its last block.
+//                   zeroes the V rows past a context's end in its last block;
+//   warps 12-15, 16-19  8-bit row caches only: fetch the codes of K and V and
+//                   convert them to q's type (prefill_convert.cuh), warp 9
+//                   streaming q alone.
 // Every wait is bounded; the tensor memory is freed on every path.
 #pragma once
 
@@ -40,6 +43,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "prefill_convert.cuh"
 #include "tc05.cuh"
 #include "tc_softmax.cuh"
 
@@ -67,6 +71,8 @@ struct DecodeTcParams {
     int slices;                       // ceil(G / 128) units per KV head
     int rows;                         // min(G, 128): rows of a partial slot and of the q box
     int cache_rows;                   // rows of the [NB * Hkv * bs][D] view of a cache
+    const unsigned char* k_cache;     // 8-bit row caches only (the others go through tensor maps)
+    const unsigned char* v_cache;
     uint32_t wait_limit;              // polls before a wait for progress gives up
 };
 
@@ -77,13 +83,14 @@ struct DecodeTcParams {
 #define PKV_DECODE_TC_VST128 2
 #endif
 
-template <typename T, int D, int BS>
+template <typename T, typename TC, int D, int BS>
 struct DecodeTcShape {
+    static constexpr bool kConvert = !std::is_same<T, TC>::value;   // 8-bit row caches
     static constexpr int M = 128;               // rows (query heads) per tile
     static constexpr int N = 128;               // keys per tile
     static constexpr int DH = D / 64;           // 64-dim halves (one 128-byte swizzle row each)
     static constexpr int BPT = N / BS;          // cache blocks per key tile
-    static constexpr int KST = D == 64 ? 5 : PKV_DECODE_TC_KST128;   // K stages
+    static constexpr int KST = D == 64 ? 5 : kConvert ? 2 : PKV_DECODE_TC_KST128;   // K stages
     static constexpr int VST = D == 64 ? 4 : PKV_DECODE_TC_VST128;   // V stages
     static constexpr uint32_t Q_HALF = M * 128;
     static constexpr uint32_t KV_HALF = N * 128;
@@ -91,8 +98,14 @@ struct DecodeTcShape {
     static constexpr uint32_t KV_BYTES = DH * KV_HALF;       // K or V of one key tile
     static constexpr uint32_t OFF_K = 2 * Q_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + KST * KV_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_V + VST * KV_BYTES;
-    static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;  // barriers, scratch, 1 KB alignment slack
+    static constexpr uint32_t OFF_STG = OFF_V + VST * KV_BYTES;     // 8-bit rows: 4 warps x (K slot, V slot)
+    static constexpr uint32_t STG_SLOT = kConvert ? 32 / BS * cache_tile_bytes<TC>(D, BS) : 0;
+    static constexpr uint32_t OFF_BAR = OFF_STG + 8 * STG_SLOT;
+    // barriers (256 bytes), tensor-memory address, scratch (320 ..), staging
+    // barriers (416 ..); 1 KB alignment slack
+    static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+    static constexpr int kSoftmaxRegs = 144, kIssueRegs = 64, kConvertRegs = 64;
+    static_assert(2 * kSoftmaxRegs + kIssueRegs + 2 * kConvertRegs <= 5 * 96, "registers of the 640 threads at launch");
     static constexpr uint32_t TM_TILE = 256;                // columns per half
     static constexpr uint32_t TM_S = 0;                     // S (N fp32 columns); P over its first N/2
     static constexpr uint32_t TM_O = N;                     // O at columns N .. N + D
@@ -103,7 +116,9 @@ struct DecodeTcShape {
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
-constexpr uint32_t kDecodeTcThreads = 352;
+// (8-bit rows: the registers of 640 threads are shared out as in the prefill kernel)
+template <typename T, typename TC>
+constexpr uint32_t kDecodeTcThreads = std::is_same<T, TC>::value ? 352 : 640;
 
 // Key tiles of one unit of sequence s (0 for an empty or invalid length).
 __device__ __forceinline__ int tc_seq_len(const DecodeTcParams& p, int s) {
@@ -144,15 +159,18 @@ struct TcSegWalk {
     }
 };
 
-template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kDecodeTcThreads, 1)
+// T: element type of q; TC: element type of the caches (T or fp8row)
+template <typename T, typename TC, int D, int BS>
+__global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
     paged_decode_tc_kernel(const DecodeTcParams p, const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-    using S = DecodeTcShape<T, D, BS>;
+    using S = DecodeTcShape<T, TC, D, BS>;
     using namespace tcsm;
     constexpr int KST = S::KST, VST = S::VST;
     constexpr int N = S::N;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kConvert = S::kConvert;
+    constexpr uint32_t kFullArrivals = kConvert ? 4 : 1;   // the converting warps, or the TMA thread
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_s = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
@@ -180,18 +198,19 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
     const uint32_t bar_vz = bar + 8 * (B0 + 8);
     const uint32_t bar_fin = bar + 8 * (B0 + 9);
     uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + S::OFF_BAR + 256);
-    int* scratch = reinterpret_cast<int*>(smem + S::OFF_BAR + 320);   // [0..15] warp sums, [16..19] start
+    int* scratch = reinterpret_cast<int*>(smem + S::OFF_BAR + 320);   // [0..19] warp sums, [20..22] start
+    auto bar_stg = [&](int w, int v) { return bar + 416 + 8 * (2 * w + v); };   // 8-bit rows: a staging slot filled
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_qfull(b), 1);
             mbar_init(bar_qempty(b), 1);
         }
         for (int st = 0; st < KST; ++st) {
-            mbar_init(bar_kfull(st), 1);
+            mbar_init(bar_kfull(st), kFullArrivals);
             mbar_init(bar_kempty(st), 1);
         }
         for (int st = 0; st < VST; ++st) {
-            mbar_init(bar_vfull(st), 1);
+            mbar_init(bar_vfull(st), kFullArrivals);
             mbar_init(bar_vempty(st), 1);
         }
         for (int x = 0; x < 2; ++x) {
@@ -202,12 +221,16 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
         }
         mbar_init(bar_vz, 1);
         mbar_init(bar_fin, 1);
+        if constexpr (kConvert)
+            for (int k = 0; k < 8; ++k) mbar_init(bar_stg(k >> 1, k & 1), 1);
         fence_mbar_init();
     }
     if (threadIdx.x == 32) {
         tc05::prefetch_tmap(&tm_q);
-        tc05::prefetch_tmap(&tm_k);
-        tc05::prefetch_tmap(&tm_v);
+        if constexpr (!kConvert) {
+            tc05::prefetch_tmap(&tm_k);
+            tc05::prefetch_tmap(&tm_v);
+        }
     }
     if (warp == 0) {
         tc05::tmem_alloc(smem_addr(tm_holder), S::TM_COLS);
@@ -260,9 +283,9 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
     // the CTA whose range holds cost index v0 in sequence s (prefix pre, cost w) notes it
     auto note_start = [&](int s, int64_t pre, int w, int64_t v0) {
         if (w > 0 && pre * NU <= v0 && v0 < (pre + w) * NU) {
-            scratch[16] = s;
-            scratch[17] = (int)(v0 - pre * NU);         // offset of the start in s's units
-            scratch[18] = (int)pre;
+            scratch[20] = s;
+            scratch[21] = (int)(v0 - pre * NU);         // offset of the start in s's units
+            scratch[22] = (int)pre;
         }
     };
     int64_t v0, v1;
@@ -277,7 +300,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
             if (lane >= off) incl += v;
         }
         if (lane == 31) scratch[warp] = incl;
-        if (threadIdx.x == 0) scratch[16] = -1;
+        if (threadIdx.x == 0) scratch[20] = -1;
         __syncthreads();
         int before = 0, all = 0;
         for (int wp = 0; wp < nwarps; ++wp) {
@@ -300,7 +323,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
         const int64_t vtot = total * NU;
         v0 = vtot * c / C;
         v1 = vtot * (c + 1) / C;
-        if (threadIdx.x == 0) scratch[16] = -1;
+        if (threadIdx.x == 0) scratch[20] = -1;
         __syncthreads();
         int64_t carry = 0;
         for (int base = 0; base < p.num_seqs; base += nthreads) {
@@ -325,7 +348,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
                 note_start(s, pre, w, v0);
             }
             carry += chunk;
-            const bool found = __syncthreads_or(scratch[16] >= 0);
+            const bool found = __syncthreads_or(scratch[20] >= 0);
             if (found && c != 0) break;
         }
         if (c == 0 && threadIdx.x == 0) p.prefix[p.num_seqs] = (int32_t)carry;
@@ -334,15 +357,15 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
     TcSegWalk walk0;
     walk0.NU = NU;
     bool has_work = false;
-    if (v1 > v0 && scratch[16] >= 0) {
-        walk0.s = scratch[16];
+    if (v1 > v0 && scratch[20] >= 0) {
+        walk0.s = scratch[20];
         walk0.L = tc_seq_len(p, walk0.s);
         walk0.Ts = (walk0.L + 127) / 128;
-        const int w = walk0.Ts + kTcUnitCost, o = scratch[17];
+        const int w = walk0.Ts + kTcUnitCost, o = scratch[21];
         walk0.u = o / w;
         walk0.t = max(0, o - walk0.u * w - kTcUnitCost);
         // the range ends at most one range length past the unit's first tile
-        walk0.left = (int)(v1 - ((int64_t)scratch[18] * NU + (int64_t)walk0.u * w + kTcUnitCost));
+        walk0.left = (int)(v1 - ((int64_t)scratch[22] * NU + (int64_t)walk0.u * w + kTcUnitCost));
         has_work = walk0.t < walk0.left;
     } else {
         walk0.s = walk0.u = walk0.t = walk0.L = walk0.Ts = walk0.left = 0;
@@ -358,191 +381,275 @@ __global__ void __launch_bounds__(kDecodeTcThreads, 1)
 
     if (!has_work) {
         // no tile in the range (more CTAs than work): nothing to do
-    } else if (warp >= 9) {
-        // ===================== TMA producers: warp 9 q and K, warp 10 V =====================
-        const bool is_v = warp == 10;
-        const int nst = is_v ? VST : KST;
-        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-        TcSegWalk w = walk0;
-        int jt = 0, js = 0, qloads[2] = {0, 0};
-        bool ok = true;
-        // V rows of the pending tile past its context end, zeroed once it lands
-        int vz_jt = -1, vz_r0 = 0, vz_r1 = 0;
-        auto do_vz = [&]() {
-            const int st = vz_jt % VST;
-            if (warp_wait(bar_vfull(st), (vz_jt / VST) & 1, wl)) {
-                const int rows = vz_r1 - vz_r0;
-                for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
-                    const int dh = i / (rows * 8);
-                    const int rem = i - dh * rows * 8;
-                    *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
-                                              (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    } else if (kConvert && warp >= 12) {
+        // ===================== converting producers: warps 12-15 K, warps 16-19 V =====================
+        if constexpr (kConvert) {
+            reg_dec<S::kConvertRegs>();
+            using Slice = SliceConverter<T, TC, D, BS>;
+            constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
+            static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
+            const int wi = (warp - 12) & 3, v = (warp - 12) >> 2;   // slice, stream (0: K, 1: V)
+            const Slice conv(wi, lane);
+            const uint32_t slot = sm + S::OFF_STG + (2 * wi + v) * S::STG_SLOT, landed = bar_stg(wi, v);
+            const unsigned char* cache = v ? p.v_cache : p.k_cache;
+            const int nst = v ? VST : KST;
+            bool ok = true;
+            int jt = 0, copies = 0;              // key tiles converted; copies requested into the slot
+            // the tile whose copies are requested next: the i-th of its segment
+            TcSegWalk walk = walk0;
+            int s, u, t0, n, L, Ts, i = 0, ids = -1;
+            int phys[BPW];
+            uint32_t missing = 0;
+            bool more = walk.next(p, s, u, t0, n, L, Ts);
+            // lane l holds the id of block l % BPW of the slice of tile l / BPW of a run of TPE tiles
+            auto request = [&]() {
+                if (i % TPE == 0) {
+                    const int lb = (t0 + i + lane / BPW) * S::BPT + wi * BPW + lane % BPW;
+                    ids = -1;
+                    if (lb < (L + BS - 1) / BS) {
+                        ids = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
+                        if (ids < 0 || ids >= p.num_blocks) {
+                            ids = -1;
+                            flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                        }
+                    }
                 }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_vz);
-            } else {
-                ok = false;
-            }
-            vz_jt = -1;
-        };
-        int s, u, t0, n, L, Ts;
-        while (ok && w.next(p, s, u, t0, n, L, Ts)) {
-            const int g = u / p.slices, sl = u - g * p.slices;
-            if (!is_v) {
-                // q of the unit into buffer js % 2, once the QKs of unit js - 2 are done
-                const int b = js & 1;
-                if (js >= 2 && !warp_wait(bar_qempty(b), ((js >> 1) - 1) & 1, wl)) { ok = false; break; }
+                missing = 0;
+#pragma unroll
+                for (int b = 0; b < BPW; ++b) {
+                    phys[b] = __shfl_sync(kAll, ids, (i % TPE) * BPW + b);
+                    if (phys[b] < 0) missing |= 1u << b;
+                }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar_qfull(b), (uint32_t)(S::DH * GR * 128));
-                    for (int dh = 0; dh < S::DH; ++dh)
-                        tc05::tma_load_3d(q_base(b) + dh * S::Q_HALF, &tm_q, dh * 64, g * G + sl * S::M, s,
-                                          bar_qfull(b));
+                    const int g = u / p.slices;
+                    uint32_t bytes = 0;
+#pragma unroll
+                    for (int b = 0; b < BPW; ++b) bytes += phys[b] >= 0 ? Slice::TILE : 0;
+                    mbar_arrive_expect_tx(landed, bytes);
+#pragma unroll
+                    for (int b = 0; b < BPW; ++b)
+                        if (phys[b] >= 0)
+                            bulk_g2s(slot + b * Slice::TILE,
+                                     cache + ((size_t)phys[b] * p.num_kv_heads + g) * Slice::TILE, Slice::TILE, landed);
                 }
-                ++qloads[b];
-            }
-            const int nblk = (L + BS - 1) / BS;
-            // cache row of block `lane` of the segment's tile i (one coalesced load
-            // per tile, a tile ahead of its copies); past the sequence's blocks, or
-            // for a bad id, the row past the pool, which TMA fills with zeros
-            auto tile_row = [&](int i) -> int {
-                int row = p.cache_rows;
-                const int lb = (t0 + i) * S::BPT + lane;
-                if (lane < S::BPT && lb < nblk) {
-                    const int phys = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
-                    if (phys >= 0 && phys < p.num_blocks) row = (phys * p.num_kv_heads + g) * BS;
-                    else if (!is_v) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                }
-                return row;
+                ++copies;
             };
-            int next_row = tile_row(0);
-            for (int i = 0; i < n; ++i, ++jt) {
-                const int cur_row = next_row;
-                if (i + 1 < n) next_row = tile_row(i + 1);
+            if (more) request();
+            for (; jt < copies; ++jt) {
                 const int st = jt % nst;
-                // the pending zeroing must happen before its stage is waited for again
-                if (is_v && vz_jt >= 0 && jt >= vz_jt + VST) do_vz();
-                if (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
+                if (!warp_wait(landed, jt & 1, wl) ||
+                    (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = is_v ? bar_vfull(st) : bar_kfull(st);
-                const uint32_t dst = is_v ? v_base(st) : k_base(st);
-                if (lane == 0) mbar_arrive_expect_tx(full, S::KV_BYTES);
-#pragma unroll
-                for (int bi = 0; bi < S::BPT; ++bi) {
-                    const int row = __shfl_sync(kAll, cur_row, bi);
-                    if (lane == 0)
-                        for (int dh = 0; dh < S::DH; ++dh)
-                            tc05::tma_load_2d(dst + dh * S::KV_HALF + bi * BS * 128, map, dh * 64, row, full);
+                conv.run(slot, v ? v_base(st) : k_base(st), L - (t0 + i) * N - 32 * wi, missing, lane);
+                fence_proxy_async();             // before the tensor core reads the tile
+                __syncwarp();                    // (and every lane is done with the slot)
+                if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
+                if (++i == n) {
+                    more = walk.next(p, s, u, t0, n, L, Ts);
+                    i = 0;
                 }
-                if (is_v && t0 + i == Ts - 1) {
-                    // the unit's last tile: V rows from the context end to the end of
-                    // its last block hold whatever the pool holds there
-                    const int r0 = L - (Ts - 1) * N;
-                    const int r1 = min(nblk * BS - (Ts - 1) * N, N);
-                    if (r0 < r1) {
-                        if (vz_jt >= 0) do_vz();
-                        vz_jt = jt;
-                        vz_r0 = r0;
-                        vz_r1 = r1;
-                    }
-                }
+                if (more) request();
             }
-            ++js;
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+            // the last copy lands before this warp leaves
+            if (copies > 0) mbar_wait_bounded(landed, (copies - 1) & 1, kWaitLimit);
+            __syncwarp();
         }
-        if (is_v && vz_jt >= 0 && ok) do_vz();
-        if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-        if (lane == 0) {
-            // every copy requested above lands before this warp leaves (the last
-            // copy into each stage and each q buffer; earlier ones were consumed
-            // before their buffer was refilled)
-            for (int b = 0; b < 2; ++b)
-                if (qloads[b] > 0) mbar_wait_bounded(bar_qfull(b), (qloads[b] - 1) & 1, kWaitLimit);
-            for (int t = max(0, jt - nst); t < jt; ++t)
-                mbar_wait_bounded(is_v ? bar_vfull(t % nst) : bar_kfull(t % nst), (t / nst) & 1, kWaitLimit);
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ===================== MMA issue =====================
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = tc05::instr_desc(kBf16, 128, N, false, false);
-            constexpr uint32_t idesc_pv = tc05::instr_desc(kBf16, 128, D, false, true);
-            // operand descriptors of q buffer 0 and stage 0; the start-address
-            // field (bits 0-13, address / 16) is advanced by plain addition
-            const uint64_t dq = tc05::smem_desc(q_base(0), 16, 1024);
-            const uint64_t dk = tc05::smem_desc(k_base(0), 16, 1024);
-            const uint64_t dv = tc05::smem_desc(v_base(0), S::KV_HALF, 1024);
+    } else if (warp >= 8) {
+        if constexpr (kConvert) reg_dec<S::kIssueRegs>();
+        if (warp == 8) {
+            // ===================== MMA issue =====================
+            if (lane == 0) {
+                constexpr uint32_t idesc_qk = tc05::instr_desc(kBf16, 128, N, false, false);
+                constexpr uint32_t idesc_pv = tc05::instr_desc(kBf16, 128, D, false, true);
+                // operand descriptors of q buffer 0 and stage 0; the start-address
+                // field (bits 0-13, address / 16) is advanced by plain addition
+                const uint64_t dq = tc05::smem_desc(q_base(0), 16, 1024);
+                const uint64_t dk = tc05::smem_desc(k_base(0), 16, 1024);
+                const uint64_t dv = tc05::smem_desc(v_base(0), S::KV_HALF, 1024);
+                TcSegWalk w = walk0;
+                bool ok = true;
+                int jt = 0, js = 0, vzc = 0;
+                int px[2] = {0, 0};                          // P_x phases consumed
+                int ox[2] = {0, 0};                          // units whose O_x accumulation began
+                struct Pend { int jt, x, first, last, vz; } prev = {-1, 0, 0, 0, 0};
+                auto pv = [&](const Pend& e) -> bool {       // O_x += P_x V_jt
+                    const int sv = e.jt % VST;
+                    if (!mbar_wait_bounded(bar_vfull(sv), (e.jt / VST) & 1, wl)) return false;
+                    if (e.vz) {
+                        if (!mbar_wait_bounded(bar_vz, vzc & 1, wl)) return false;
+                        ++vzc;
+                    }
+                    if (!mbar_wait_bounded(bar_p(e.x), px[e.x] & 1, wl)) return false;
+                    ++px[e.x];
+                    if (e.first) {
+                        // the half's previous unit must be read out before O_x restarts
+                        if (ox[e.x] >= 1 && !mbar_wait_bounded(bar_ofree(e.x), (ox[e.x] - 1) & 1, wl)) return false;
+                        ++ox[e.x];
+                    }
+                    tc05::fence_after_sync();
+                    const uint32_t base = tm + e.x * S::TM_TILE;
+                    const uint64_t vd = dv + (uint64_t)((sv * S::KV_BYTES) >> 4);
+                    // k-th 16 keys: 16 rows of 128 bytes further; P pairs 8 columns further
+    #pragma unroll
+                    for (int k = 0; k < N / 16; ++k)
+                        tc05::mma_ts(base + S::TM_O, base + S::TM_S + 8 * k, vd + (uint64_t)(k * 128), idesc_pv,
+                                     (!e.first || k > 0) ? 1u : 0u);
+                    tc05::commit(bar_vempty(sv));
+                    if (e.last) tc05::commit(bar_o(e.x));
+                    return true;
+                };
+                int s, u, t0, n, L, Ts;
+                while (ok && w.next(p, s, u, t0, n, L, Ts)) {
+                    const int b = js & 1;
+                    if (!mbar_wait_bounded(bar_qfull(b), (js >> 1) & 1, wl)) { ok = false; break; }
+                    const int nblk = (L + BS - 1) / BS;
+                    const bool unit_vz = !kConvert && t0 + n == Ts && L - (Ts - 1) * N < min(nblk * BS - (Ts - 1) * N, N);
+                    for (int i = 0; i < n; ++i, ++jt) {
+                        const int x = jt & 1;
+                        if (!mbar_wait_bounded(bar_kfull(jt % KST), (jt / KST) & 1, wl)) { ok = false; break; }
+                        tc05::fence_after_sync();
+                        {                                    // S_x = q K_jt^T
+                            const uint32_t d = tm + x * S::TM_TILE + S::TM_S;
+                            const uint64_t ad = dq + (uint64_t)((b * S::Q_BYTES) >> 4);
+                            const uint64_t bd = dk + (uint64_t)(((jt % KST) * S::KV_BYTES) >> 4);
+                            // k-th 16-wide slice: +32 bytes inside a swizzle row, next half after 4
+    #pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t qoff = ((k >> 2) * S::Q_HALF + (k & 3) * 32) >> 4;
+                                const uint32_t koff = ((k >> 2) * S::KV_HALF + (k & 3) * 32) >> 4;
+                                tc05::mma_ss(d, ad + qoff, bd + koff, idesc_qk, k > 0 ? 1u : 0u);
+                            }
+                        }
+                        tc05::commit(bar_s(x));
+                        tc05::commit(bar_kempty(jt % KST));
+                        if (i == n - 1) tc05::commit(bar_qempty(b));
+                        if (prev.jt >= 0 && !pv(prev)) { ok = false; break; }
+                        // this tile's half: its first tile of the unit are i = 0, 1, its last i = n-2, n-1
+                        prev = {jt, x, i < 2 ? 1 : 0, i >= n - 2 ? 1 : 0, (unit_vz && i == n - 1) ? 1 : 0};
+                    }
+                    ++js;
+                }
+                if (ok && prev.jt >= 0 && !pv(prev)) ok = false;
+                if (!ok) flag_error(p.errors, PKV_DEVERR_WAIT);
+                // every MMA issued above is complete before the tensor memory is freed
+                tc05::commit(bar_fin);
+                mbar_wait_bounded(bar_fin, 0, kWaitLimit);
+            }
+        } else if (!kConvert || warp == 9) {
+            // ===================== TMA producers: warp 9 q and K, warp 10 V =====================
+            const bool is_v = warp == 10;
+            const int nst = is_v ? VST : KST;
+            const CUtensorMap* map = is_v ? &tm_v : &tm_k;
             TcSegWalk w = walk0;
+            int jt = 0, js = 0, qloads[2] = {0, 0};
             bool ok = true;
-            int jt = 0, js = 0, vzc = 0;
-            int px[2] = {0, 0};                          // P_x phases consumed
-            int ox[2] = {0, 0};                          // units whose O_x accumulation began
-            struct Pend { int jt, x, first, last, vz; } prev = {-1, 0, 0, 0, 0};
-            auto pv = [&](const Pend& e) -> bool {       // O_x += P_x V_jt
-                const int sv = e.jt % VST;
-                if (!mbar_wait_bounded(bar_vfull(sv), (e.jt / VST) & 1, wl)) return false;
-                if (e.vz) {
-                    if (!mbar_wait_bounded(bar_vz, vzc & 1, wl)) return false;
-                    ++vzc;
+            // V rows of the pending tile past its context end, zeroed once it lands
+            int vz_jt = -1, vz_r0 = 0, vz_r1 = 0;
+            auto do_vz = [&]() {
+                const int st = vz_jt % VST;
+                if (warp_wait(bar_vfull(st), (vz_jt / VST) & 1, wl)) {
+                    const int rows = vz_r1 - vz_r0;
+                    for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
+                        const int dh = i / (rows * 8);
+                        const int rem = i - dh * rows * 8;
+                        *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
+                                                  (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_vz);
+                } else {
+                    ok = false;
                 }
-                if (!mbar_wait_bounded(bar_p(e.x), px[e.x] & 1, wl)) return false;
-                ++px[e.x];
-                if (e.first) {
-                    // the half's previous unit must be read out before O_x restarts
-                    if (ox[e.x] >= 1 && !mbar_wait_bounded(bar_ofree(e.x), (ox[e.x] - 1) & 1, wl)) return false;
-                    ++ox[e.x];
-                }
-                tc05::fence_after_sync();
-                const uint32_t base = tm + e.x * S::TM_TILE;
-                const uint64_t vd = dv + (uint64_t)((sv * S::KV_BYTES) >> 4);
-                // k-th 16 keys: 16 rows of 128 bytes further; P pairs 8 columns further
-#pragma unroll
-                for (int k = 0; k < N / 16; ++k)
-                    tc05::mma_ts(base + S::TM_O, base + S::TM_S + 8 * k, vd + (uint64_t)(k * 128), idesc_pv,
-                                 (!e.first || k > 0) ? 1u : 0u);
-                tc05::commit(bar_vempty(sv));
-                if (e.last) tc05::commit(bar_o(e.x));
-                return true;
+                vz_jt = -1;
             };
             int s, u, t0, n, L, Ts;
             while (ok && w.next(p, s, u, t0, n, L, Ts)) {
-                const int b = js & 1;
-                if (!mbar_wait_bounded(bar_qfull(b), (js >> 1) & 1, wl)) { ok = false; break; }
+                const int g = u / p.slices, sl = u - g * p.slices;
+                if (!is_v) {
+                    // q of the unit into buffer js % 2, once the QKs of unit js - 2 are done
+                    const int b = js & 1;
+                    if (js >= 2 && !warp_wait(bar_qempty(b), ((js >> 1) - 1) & 1, wl)) { ok = false; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar_qfull(b), (uint32_t)(S::DH * GR * 128));
+                        for (int dh = 0; dh < S::DH; ++dh)
+                            tc05::tma_load_3d(q_base(b) + dh * S::Q_HALF, &tm_q, dh * 64, g * G + sl * S::M, s,
+                                              bar_qfull(b));
+                    }
+                    ++qloads[b];
+                }
+                if constexpr (kConvert) {
+                    ++js;
+                    continue;
+                }
                 const int nblk = (L + BS - 1) / BS;
-                const bool unit_vz = t0 + n == Ts && L - (Ts - 1) * N < min(nblk * BS - (Ts - 1) * N, N);
+                // cache row of block `lane` of the segment's tile i (one coalesced load
+                // per tile, a tile ahead of its copies); past the sequence's blocks, or
+                // for a bad id, the row past the pool, which TMA fills with zeros
+                auto tile_row = [&](int i) -> int {
+                    int row = p.cache_rows;
+                    const int lb = (t0 + i) * S::BPT + lane;
+                    if (lane < S::BPT && lb < nblk) {
+                        const int phys = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + lb);
+                        if (phys >= 0 && phys < p.num_blocks) row = (phys * p.num_kv_heads + g) * BS;
+                        else if (!is_v) flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                    }
+                    return row;
+                };
+                int next_row = tile_row(0);
                 for (int i = 0; i < n; ++i, ++jt) {
-                    const int x = jt & 1;
-                    if (!mbar_wait_bounded(bar_kfull(jt % KST), (jt / KST) & 1, wl)) { ok = false; break; }
-                    tc05::fence_after_sync();
-                    {                                    // S_x = q K_jt^T
-                        const uint32_t d = tm + x * S::TM_TILE + S::TM_S;
-                        const uint64_t ad = dq + (uint64_t)((b * S::Q_BYTES) >> 4);
-                        const uint64_t bd = dk + (uint64_t)(((jt % KST) * S::KV_BYTES) >> 4);
-                        // k-th 16-wide slice: +32 bytes inside a swizzle row, next half after 4
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t qoff = ((k >> 2) * S::Q_HALF + (k & 3) * 32) >> 4;
-                            const uint32_t koff = ((k >> 2) * S::KV_HALF + (k & 3) * 32) >> 4;
-                            tc05::mma_ss(d, ad + qoff, bd + koff, idesc_qk, k > 0 ? 1u : 0u);
+                    const int cur_row = next_row;
+                    if (i + 1 < n) next_row = tile_row(i + 1);
+                    const int st = jt % nst;
+                    // the pending zeroing must happen before its stage is waited for again
+                    if (is_v && vz_jt >= 0 && jt >= vz_jt + VST) do_vz();
+                    if (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = is_v ? bar_vfull(st) : bar_kfull(st);
+                    const uint32_t dst = is_v ? v_base(st) : k_base(st);
+                    if (lane == 0) mbar_arrive_expect_tx(full, S::KV_BYTES);
+    #pragma unroll
+                    for (int bi = 0; bi < S::BPT; ++bi) {
+                        const int row = __shfl_sync(kAll, cur_row, bi);
+                        if (lane == 0)
+                            for (int dh = 0; dh < S::DH; ++dh)
+                                tc05::tma_load_2d(dst + dh * S::KV_HALF + bi * BS * 128, map, dh * 64, row, full);
+                    }
+                    if (is_v && t0 + i == Ts - 1) {
+                        // the unit's last tile: V rows from the context end to the end of
+                        // its last block hold whatever the pool holds there
+                        const int r0 = L - (Ts - 1) * N;
+                        const int r1 = min(nblk * BS - (Ts - 1) * N, N);
+                        if (r0 < r1) {
+                            if (vz_jt >= 0) do_vz();
+                            vz_jt = jt;
+                            vz_r0 = r0;
+                            vz_r1 = r1;
                         }
                     }
-                    tc05::commit(bar_s(x));
-                    tc05::commit(bar_kempty(jt % KST));
-                    if (i == n - 1) tc05::commit(bar_qempty(b));
-                    if (prev.jt >= 0 && !pv(prev)) { ok = false; break; }
-                    // this tile's half: its first tile of the unit are i = 0, 1, its last i = n-2, n-1
-                    prev = {jt, x, i < 2 ? 1 : 0, i >= n - 2 ? 1 : 0, (unit_vz && i == n - 1) ? 1 : 0};
                 }
                 ++js;
             }
-            if (ok && prev.jt >= 0 && !pv(prev)) ok = false;
-            if (!ok) flag_error(p.errors, PKV_DEVERR_WAIT);
-            // every MMA issued above is complete before the tensor memory is freed
-            tc05::commit(bar_fin);
-            mbar_wait_bounded(bar_fin, 0, kWaitLimit);
+            if (is_v && vz_jt >= 0 && ok) do_vz();
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+            if (lane == 0) {
+                // every copy requested above lands before this warp leaves (the last
+                // copy into each stage and each q buffer; earlier ones were consumed
+                // before their buffer was refilled)
+                for (int b = 0; b < 2; ++b)
+                    if (qloads[b] > 0) mbar_wait_bounded(bar_qfull(b), (qloads[b] - 1) & 1, kWaitLimit);
+                for (int t = max(0, jt - nst); t < jt; ++t)
+                    mbar_wait_bounded(is_v ? bar_vfull(t % nst) : bar_kfull(t % nst), (t / nst) & 1, kWaitLimit);
+            }
+            __syncwarp();
         }
     } else {
+        if constexpr (kConvert) reg_inc<S::kSoftmaxRegs>();
         // ===================== softmax and partials: one row (query head) per thread =====================
         const int x = warp >> 2;                        // half
         const int wq = warp & 3;

@@ -244,7 +244,8 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     // over an FP8 cache the warps retire blocks twice as fast, so longer
     // partitions leave too few items per warp: at most 32 blocks there
     if (fp8_cache && ps_hi > 32 * block_size) ps_hi = 32 * block_size;
-    const bool tc = !fp8_cache && app == nullptr && use_decode_tc(num_heads, num_kv_heads, dtype, partition_size);
+    const bool tc = kind != pkv::CacheKind::kFp8 && app == nullptr &&
+                    use_decode_tc(num_heads, num_kv_heads, dtype, partition_size);
     const WorkspaceLayout wl =
         workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, ps, tc);
     if (!workspace || !aligned16(workspace) || workspace_bytes < wl.total) return PKV_ERR_WORKSPACE;
@@ -277,6 +278,7 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
         a.max_blocks_per_seq = max_blocks_per_seq;
         a.max_context_len = max_context_len;
         a.dtype = dtype;
+        a.kind = kind;
         a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
         return pkv::launch_decode_tc(a, static_cast<cudaStream_t>(stream));
     }

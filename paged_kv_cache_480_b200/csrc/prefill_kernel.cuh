@@ -134,8 +134,6 @@ struct PrefillShape {
 template <typename T, typename TC>
 constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 640;
 
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // One work item as the scheduler hands it to the other roles.
 struct PrefillItem {
