@@ -90,20 +90,24 @@ struct DecodeTcShape {
     static constexpr int N = 128;               // keys per tile
     static constexpr int DH = D / 64;           // 64-dim halves (one 128-byte swizzle row each)
     static constexpr int BPT = N / BS;          // cache blocks per key tile
-    static constexpr int KST = D == 64 ? 5 : kConvert ? 2 : PKV_DECODE_TC_KST128;   // K stages
-    static constexpr int VST = D == 64 ? 4 : PKV_DECODE_TC_VST128;   // V stages
+    // K and V stages.  8-bit rows: what hides the memory latency is the codes in
+    // flight, so the room goes to NS staging slots a warp (33 KB a tile at 128
+    // dims; one slot: 1.9 TB/s) and one converted tile of each stream.
+    static constexpr int KST = kConvert ? (D == 64 ? 3 : 1) : D == 64 ? 5 : PKV_DECODE_TC_KST128;
+    static constexpr int VST = kConvert ? (D == 64 ? 3 : 1) : D == 64 ? 4 : PKV_DECODE_TC_VST128;
+    static constexpr int NS = D == 64 ? 5 : 3;
     static constexpr uint32_t Q_HALF = M * 128;
     static constexpr uint32_t KV_HALF = N * 128;
     static constexpr uint32_t Q_BYTES = DH * Q_HALF;         // one q buffer
     static constexpr uint32_t KV_BYTES = DH * KV_HALF;       // K or V of one key tile
     static constexpr uint32_t OFF_K = 2 * Q_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + KST * KV_BYTES;
-    static constexpr uint32_t OFF_STG = OFF_V + VST * KV_BYTES;     // 8-bit rows: 4 warps x (K slot, V slot)
+    static constexpr uint32_t OFF_STG = OFF_V + VST * KV_BYTES;     // 8-bit rows: (4 K warps, 4 V warps) x NS slots
     static constexpr uint32_t STG_SLOT = kConvert ? 32 / BS * cache_tile_bytes<TC>(D, BS) : 0;
-    static constexpr uint32_t OFF_BAR = OFF_STG + 8 * STG_SLOT;
+    static constexpr uint32_t OFF_BAR = OFF_STG + 8 * NS * STG_SLOT;
     // barriers (256 bytes), tensor-memory address, scratch (320 ..), staging
     // barriers (416 ..); 1 KB alignment slack
-    static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+    static constexpr uint32_t SMEM = OFF_BAR + (kConvert ? 416 + 64 * NS : 512) + 1024;
     static constexpr int kSoftmaxRegs = 144, kIssueRegs = 64, kConvertRegs = 64;
     static_assert(2 * kSoftmaxRegs + kIssueRegs + 2 * kConvertRegs <= 5 * 96, "registers of the 640 threads at launch");
     static constexpr uint32_t TM_TILE = 256;                // columns per half
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
     const uint32_t bar_fin = bar + 8 * (B0 + 9);
     uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + S::OFF_BAR + 256);
     int* scratch = reinterpret_cast<int*>(smem + S::OFF_BAR + 320);   // [0..19] warp sums, [20..22] start
-    auto bar_stg = [&](int w, int v) { return bar + 416 + 8 * (2 * w + v); };   // 8-bit rows: a staging slot filled
+    auto bar_stg = [&](int k) { return bar + 416 + 8 * k; };   // 8-bit rows: staging slot k filled
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_qfull(b), 1);
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
         mbar_init(bar_vz, 1);
         mbar_init(bar_fin, 1);
         if constexpr (kConvert)
-            for (int k = 0; k < 8; ++k) mbar_init(bar_stg(k >> 1, k & 1), 1);
+            for (int k = 0; k < 8 * S::NS; ++k) mbar_init(bar_stg(k), 1);
         fence_mbar_init();
     }
     if (threadIdx.x == 32) {
@@ -389,20 +393,22 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
             constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
             static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
             const int wi = (warp - 12) & 3, v = (warp - 12) >> 2;   // slice, stream (0: K, 1: V)
+            constexpr int NS = S::NS;
             const Slice conv(wi, lane);
-            const uint32_t slot = sm + S::OFF_STG + (2 * wi + v) * S::STG_SLOT, landed = bar_stg(wi, v);
+            const int slot0 = NS * (4 * v + wi);
+            auto slot = [&](int k) { return sm + S::OFF_STG + (slot0 + k % NS) * S::STG_SLOT; };
             const unsigned char* cache = v ? p.v_cache : p.k_cache;
             const int nst = v ? VST : KST;
             bool ok = true;
-            int jt = 0, copies = 0;              // key tiles converted; copies requested into the slot
+            int jt = 0, copies = 0;              // key tiles converted; tiles whose copies were requested
+            int info[NS];                        // of the tiles in flight, oldest first: rows | missing blocks << 8
             // the tile whose copies are requested next: the i-th of its segment
             TcSegWalk walk = walk0;
             int s, u, t0, n, L, Ts, i = 0, ids = -1;
             int phys[BPW];
-            uint32_t missing = 0;
             bool more = walk.next(p, s, u, t0, n, L, Ts);
             // lane l holds the id of block l % BPW of the slice of tile l / BPW of a run of TPE tiles
-            auto request = [&]() {
+            auto request = [&](int& note) {
                 if (i % TPE == 0) {
                     const int lb = (t0 + i + lane / BPW) * S::BPT + wi * BPW + lane % BPW;
                     ids = -1;
@@ -414,47 +420,54 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                         }
                     }
                 }
-                missing = 0;
+                note = min(max(L - (t0 + i) * N - 32 * wi, 0), 32);
 #pragma unroll
                 for (int b = 0; b < BPW; ++b) {
                     phys[b] = __shfl_sync(kAll, ids, (i % TPE) * BPW + b);
-                    if (phys[b] < 0) missing |= 1u << b;
+                    if (phys[b] < 0) note |= 256 << b;
                 }
                 if (lane == 0) {
                     const int g = u / p.slices;
                     uint32_t bytes = 0;
 #pragma unroll
                     for (int b = 0; b < BPW; ++b) bytes += phys[b] >= 0 ? Slice::TILE : 0;
+                    const uint32_t landed = bar_stg(slot0 + copies % NS), dst = slot(copies);
                     mbar_arrive_expect_tx(landed, bytes);
 #pragma unroll
                     for (int b = 0; b < BPW; ++b)
                         if (phys[b] >= 0)
-                            bulk_g2s(slot + b * Slice::TILE,
+                            bulk_g2s(dst + b * Slice::TILE,
                                      cache + ((size_t)phys[b] * p.num_kv_heads + g) * Slice::TILE, Slice::TILE, landed);
                 }
                 ++copies;
-            };
-            if (more) request();
-            for (; jt < copies; ++jt) {
-                const int st = jt % nst;
-                if (!warp_wait(landed, jt & 1, wl) ||
-                    (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
-                    ok = false;
-                    break;
-                }
-                conv.run(slot, v ? v_base(st) : k_base(st), L - (t0 + i) * N - 32 * wi, missing, lane);
-                fence_proxy_async();             // before the tensor core reads the tile
-                __syncwarp();                    // (and every lane is done with the slot)
-                if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
                 if (++i == n) {
                     more = walk.next(p, s, u, t0, n, L, Ts);
                     i = 0;
                 }
-                if (more) request();
+            };
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                info[k] = 0;
+                if (more) request(info[k]);
+            }
+            for (; jt < copies; ++jt) {
+                const int st = jt % nst;
+                if (!warp_wait(bar_stg(slot0 + jt % NS), (jt / NS) & 1, wl) ||
+                    (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
+                    ok = false;
+                    break;
+                }
+                conv.run(slot(jt), v ? v_base(st) : k_base(st), info[0] & 0xff, (uint32_t)info[0] >> 8, lane);
+                fence_proxy_async();             // before the tensor core reads the tile
+                __syncwarp();                    // (and every lane is done with the slot)
+                if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
+#pragma unroll
+                for (int k = 0; k + 1 < NS; ++k) info[k] = info[k + 1];
+                if (more) request(info[NS - 1]);
             }
             if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-            // the last copy lands before this warp leaves
-            if (copies > 0) mbar_wait_bounded(landed, (copies - 1) & 1, kWaitLimit);
+            // the copies still in flight land before this warp leaves
+            for (; jt < copies; ++jt) mbar_wait_bounded(bar_stg(slot0 + jt % NS), (jt / NS) & 1, kWaitLimit);
             __syncwarp();
         }
     } else if (warp >= 8) {

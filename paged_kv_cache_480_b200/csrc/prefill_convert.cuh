@@ -16,11 +16,17 @@
 
 namespace pkv {
 
-// Two E4M3 codes (in the high bytes of x's halves) as two bf16 values times
-// 2^-120: the code's exponent and fraction moved to the low end of bf16's
-// exponent and the top of its fraction.
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2_raw(uint32_t x) {
-    return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+// Two E4M3 codes, y = b0 | b1 << 16, as two bf16 values times 2^-120: the code's
+// exponent and fraction moved to the low end of bf16's exponent and the top of
+// its fraction, m << 4 with m = y & 0x7f, its sign (y - m) << 8: 256 y - 240 m.
+// Multiply-adds with the factors in registers, because shifts and masks share
+// the half-rate integer pipe with most of the softmax and would bind it.
+struct Bf16Factors {
+    uint32_t up = 256u, down = (uint32_t)-240;
+    __device__ __forceinline__ Bf16Factors() { asm volatile("" : "+r"(up), "+r"(down)); }
+};
+__device__ __forceinline__ uint32_t e4m3_to_bf16x2_raw(uint32_t y, const Bf16Factors& f) {
+    return (y & 0x007f007fu) * f.down + y * f.up;
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -37,7 +43,7 @@ __device__ __forceinline__ uint32_t twice16(uint32_t h) { return h | (h << 16); 
 // m is 2^e in both halves for fp16 (unused without row scales), 2^(120 + e) for
 // bf16.
 template <typename T, bool ROW>
-__device__ __forceinline__ void convert16(const uint4& c, uint32_t m, uint4& lo, uint4& hi) {
+__device__ __forceinline__ void convert16(const uint4& c, uint32_t m, const Bf16Factors& f, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t o[8];
 #pragma unroll
@@ -50,8 +56,8 @@ __device__ __forceinline__ void convert16(const uint4& c, uint32_t m, uint4& lo,
                 o[2 * i + 1] = mul_f16x2(o[2 * i + 1], m);
             }
         } else {
-            o[2 * i] = mul_bf16x2(e4m3_hi_to_bf16x2_raw(__byte_perm(w[i], 0, 0x1404)), m);
-            o[2 * i + 1] = mul_bf16x2(e4m3_hi_to_bf16x2_raw(__byte_perm(w[i], 0, 0x3424)), m);
+            o[2 * i] = mul_bf16x2(e4m3_to_bf16x2_raw(__byte_perm(w[i], 0, 0x4140), f), m);
+            o[2 * i + 1] = mul_bf16x2(e4m3_to_bf16x2_raw(__byte_perm(w[i], 0, 0x4342), f), m);
         }
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
@@ -112,6 +118,7 @@ struct SliceConverter {
     uint32_t src, sca;  // the lane's codes and scale bytes, from the slot's start
     uint32_t dst;       // its row r0 of the tile, from the tile's start
     uint32_t ch;        // first of the piece's two 16-byte columns
+    Bf16Factors factors;
 
     __device__ __forceinline__ SliceConverter(int w, int lane) {
         odd = (lane >> 2) & 1;
@@ -164,9 +171,9 @@ struct SliceConverter {
                     }
                 }
                 uint4 lo, hi;
-                convert16<T, kRow>(ca, ma, lo, hi);
+                convert16<T, kRow>(ca, ma, factors, lo, hi);
                 put(tile, j ^ odd, lo, hi);
-                convert16<T, kRow>(cb, mb, lo, hi);
+                convert16<T, kRow>(cb, mb, factors, lo, hi);
                 put(tile, (j + 1) ^ odd, lo, hi);
             }
         } else {
@@ -181,7 +188,7 @@ struct SliceConverter {
                 }
                 const bool in = b >= P::LO && b <= P::HI;
                 uint4 lo, hi;
-                convert16<T, kRow>(c, in ? P::of(b) : P::first(b), lo, hi);
+                convert16<T, kRow>(c, in ? P::of(b) : P::first(b), factors, lo, hi);
                 if constexpr (kRow) {
                     const uint32_t m2 = in ? P::kHalf ? 0x3c003c00u : 0x3f803f80u : P::second(b);
                     uint32_t* o[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
