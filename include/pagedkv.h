@@ -232,8 +232,10 @@ pkv_status reshape_and_cache_fp8kv(const void* key, const void* value, void* k_c
  * softmax weights are taken relative to the largest weight times V scale, so
  * rows of very different scales keep their precision.  With 16-bit q the
  * products run on the tensor cores in fp16 (bf16 q is rounded to fp16 there,
- * so |q| must stay below 65504).  Workspace, partitioning, checks and errors
- * as for paged_attention_decode.
+ * so |q| must stay below 65504).  With 16-bit q, G >= 17 and partition_size 0
+ * the call takes the tcgen05 kernel, in q's type: weights are rounded to it,
+ * and elements are taken in it as in paged_attention_prefill_fp8row.
+ * Workspace, partitioning, checks and errors as for paged_attention_decode.
  *
  * Scale bytes the calls never write (below 67, 188 to 254) give undefined
  * values, and codes 0x7f / 0xff occur only in NaN rows.

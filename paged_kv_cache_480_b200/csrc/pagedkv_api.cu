@@ -109,10 +109,13 @@ struct WorkspaceLayout {
 };
 
 // Whether a plain decode call takes the tensor-core split-context kernel:
-// 16-bit q and caches, at least kDecodeTcMinGroup query heads per KV head,
-// and the library's choice of partitions.
-bool use_decode_tc(int num_heads, int num_kv_heads, int dtype, int partition_size) {
-    return dtype != PKV_F32 && num_heads / num_kv_heads >= pkv::kDecodeTcMinGroup && partition_size == 0;
+// 16-bit q, 16-bit or 8-bit row caches, at least kDecodeTcMinGroup (row caches:
+// kDecodeTcMinGroupRows) query heads per KV head, and the library's choice of
+// partitions.
+bool use_decode_tc(int num_heads, int num_kv_heads, int dtype, int partition_size,
+                   pkv::CacheKind kind = pkv::CacheKind::kSame) {
+    const int least = kind == pkv::CacheKind::kFp8Row ? pkv::kDecodeTcMinGroupRows : pkv::kDecodeTcMinGroup;
+    return kind != pkv::CacheKind::kFp8 && dtype != PKV_F32 && num_heads / num_kv_heads >= least && partition_size == 0;
 }
 
 WorkspaceLayout workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int head_size,
@@ -244,8 +247,7 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     // over an FP8 cache the warps retire blocks twice as fast, so longer
     // partitions leave too few items per warp: at most 32 blocks there
     if (fp8_cache && ps_hi > 32 * block_size) ps_hi = 32 * block_size;
-    const bool tc = kind != pkv::CacheKind::kFp8 && app == nullptr &&
-                    use_decode_tc(num_heads, num_kv_heads, dtype, partition_size);
+    const bool tc = app == nullptr && use_decode_tc(num_heads, num_kv_heads, dtype, partition_size, kind);
     const WorkspaceLayout wl =
         workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, ps, tc);
     if (!workspace || !aligned16(workspace) || workspace_bytes < wl.total) return PKV_ERR_WORKSPACE;

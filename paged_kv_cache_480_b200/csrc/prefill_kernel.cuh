@@ -116,7 +116,7 @@ struct PrefillShape {
     static constexpr uint32_t OFF_ITEMS = (OFF_BAR + 8 * NBAR + 63) / 64 * 64;   // item ring, 64 bytes a slot
     static constexpr uint32_t OFF_HOLD = OFF_ITEMS + 64 * IR;                   // tensor-memory address
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;  // 1 KB alignment slack
-    static constexpr int kSoftmaxRegs = 144, kIssueRegs = 64, kConvertRegs = 64;
+    static constexpr int kSoftmaxRegs = 136, kIssueRegs = 80, kConvertRegs = 64;
     static_assert(2 * kSoftmaxRegs + kIssueRegs + 2 * kConvertRegs <= 5 * 96, "registers of the 640 threads at launch");
     static constexpr uint32_t TM_TILE = 256;                // columns per query tile
     static constexpr uint32_t TM_S = 0;                     // S (N fp32 columns); P over its first N/2
