@@ -39,9 +39,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t twice16(uint32_t h) { return h | (h << 16); }
 
-// 16 codes times the pair multiplier m, as 16-bit values: lo holds codes 0-7.
-// m is 2^e in both halves for fp16 (unused without row scales), 2^(120 + e) for
-// bf16.
+// 16 codes as 16-bit values, lo the codes 0-7; of a row cache times the pair
+// multiplier m, 2^e in both halves for fp16 and 2^(120 + e) for bf16 (rows with
+// NaN codes have a NaN multiplier, so the codes' own NaN need no care there).
 template <typename T, bool ROW>
 __device__ __forceinline__ void convert16(const uint4& c, uint32_t m, const Bf16Factors& f, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -55,6 +55,13 @@ __device__ __forceinline__ void convert16(const uint4& c, uint32_t m, const Bf16
                 o[2 * i] = mul_f16x2(o[2 * i], m);
                 o[2 * i + 1] = mul_f16x2(o[2 * i + 1], m);
             }
+        } else if constexpr (!ROW) {
+            // through fp16 and fp32: no scale to apply, and NaN codes stay NaN
+            float a0, a1, b0, b1;
+            Elem<__half>::widen2(e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu)), a0, a1);
+            Elem<__half>::widen2(e4m3x2_to_f16x2((uint16_t)(w[i] >> 16)), b0, b1);
+            o[2 * i] = Elem<__nv_bfloat16>::pack2(a0, a1);
+            o[2 * i + 1] = Elem<__nv_bfloat16>::pack2(b0, b1);
         } else {
             o[2 * i] = mul_bf16x2(e4m3_to_bf16x2_raw(__byte_perm(w[i], 0, 0x4140), f), m);
             o[2 * i + 1] = mul_bf16x2(e4m3_to_bf16x2_raw(__byte_perm(w[i], 0, 0x4342), f), m);

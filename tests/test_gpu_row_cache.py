@@ -108,6 +108,10 @@ def test_rotary_write(dt, T, H, Hkv, D, R, bs, il):
     assert (amax <= 448.0 * torch.pow(2.0, e) + s).all() and (amax > 224.0 * torch.pow(2.0, e) - s).all()
     step = torch.maximum(ref.abs() * 2.0 ** -4, 2.0 ** -10 * torch.pow(2.0, e)[..., None])
     rm.close(rm.value(c[blk, :, off], b[blk, :, off]), ref, step + 2 * slack)
+    if H:                                           # q in place: the same bits
+        q2 = q.clone()
+        pkv.rotary_reshape_and_cache_fp8row(q2, q2, k, v, kc, vc, pos, slots, f, interleaved=il, attention_scale=att)
+        assert torch.equal(q2, qo)
     # every other byte of the K pool stays
     cb, bb = rm.codes_of(before[0], bs, D)
     cb[blk, :, off] = c[blk, :, off]
@@ -165,6 +169,11 @@ def test_gather_bad_pages_and_lengths():
     assert torch.equal(k[:16], c[1].transpose(0, 1)) and (k[16:36] == 0).all()
     assert torch.equal(k[36:40], c[2].transpose(0, 1)[:4]) and torch.equal(v[40:56], c[3].transpose(0, 1))
     assert torch.equal(k[56:72], c[4].transpose(0, 1)) and (k[72:] == 7).all()      # past the table: not written
+    # rows before the first sequence stay, too
+    k.fill_(7.0)
+    pkv.gather_cache(k, v, c, c, bt[2:], torch.tensor([50, 82], dtype=torch.int32, device="cuda"))
+    assert pkv.read_device_errors() == 0
+    assert (k[:50] == 7).all() and torch.equal(k[50:66], c[3].transpose(0, 1)) and (k[82:] == 7).all()
 
 
 # ---- decode --------------------------------------------------------------------
@@ -414,6 +423,35 @@ def test_prefill_takes_elements_in_q_type(dt):
     assert (out[~fine] == same[~fine]).all()
     if dt == "bf16":
         assert fine.all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_prefill_nan_rows_and_codes(dt):
+    """A NaN row of K (V) makes the queries that see its tile NaN in its head; a
+    NaN code of a per-tensor V cache makes its dim NaN."""
+    dtype, D, bs = rm.DT[dt], 64, 16
+    kc, vc, bt, cl, gc = paged_rows([200, 40], 4, 2, D, bs, dt, 28)
+    q = torch.randn(240, 4, D, generator=gc, device="cuda").to(dtype)
+    start = torch.tensor([0, 200, 240], dtype=torch.int32, device="cuda")
+    bad = torch.ones(1, 2, D, device="cuda")
+    bad[0, 1, 3] = math.nan
+    at = torch.tensor([130 % bs], device="cuda")
+    for which in (0, 1):
+        pair = [kc.clone(), vc.clone()]
+        rm.put(pair[which], bs, D, bt[0, 130 // bs:130 // bs + 1].long(), at, bad)
+        out = torch.empty_like(q)
+        pkv.paged_attention_prefill_fp8row(out, q, *pair, bt, cl, start, 0.125, max_query_len=200)
+        assert out[130:200, 2:].isnan().all() and out[:128].isfinite().all()
+        assert out[:, :2].isfinite().all() and out[200:].isfinite().all()
+    k8, v8 = (torch.full((bt.max() + 1, 2, bs, D), 0x38, dtype=torch.uint8, device="cuda") for _ in range(2))   # 1.0
+    v8[bt[0, 0].long(), 1, 5, 7] = 0xff
+    pkv.paged_attention_prefill_fp8kv(out, q, k8, v8, bt, cl, start, 0.125, 1.0, 1.0, max_query_len=200)
+    assert out[5:200, 2:, 7].isnan().all()
+    out[:200, 2:, 7] = 1.0
+    assert (out == 1.0).all()
+    k8[bt[0, 0].long(), 0, 5, 7] = 0x7f
+    pkv.paged_attention_prefill_fp8kv(out, q, k8, v8, bt, cl, start, 0.125, 1.0, 1.0, max_query_len=200)
+    assert out[5:200, :2].isnan().all() and out[:5, :2].isfinite().all()
 
 
 def test_prefill_checks_and_unwritten_rows():
