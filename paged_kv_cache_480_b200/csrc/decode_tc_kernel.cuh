@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
             static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
             const int wi = (warp - 12) & 3, v = (warp - 12) >> 2;   // slice, stream (0: K, 1: V)
             constexpr int NS = S::NS;
-            const Slice conv(wi, lane);
+            const Slice conv(lane);
             const int slot0 = NS * (4 * v + wi);
             auto slot = [&](int k) { return sm + S::OFF_STG + (slot0 + k % NS) * S::STG_SLOT; };
             const unsigned char* cache = v ? p.v_cache : p.k_cache;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                     ok = false;
                     break;
                 }
-                conv.run(slot(jt), v ? v_base(st) : k_base(st), info[0] & 0xff, (uint32_t)info[0] >> 8, lane);
+                conv.run(slot(jt), (v ? v_base(st) : k_base(st)) + wi * (32 * 128), info[0] & 0xff, (uint32_t)info[0] >> 8, lane);
                 fence_proxy_async();             // before the tensor core reads the tile
                 __syncwarp();                    // (and every lane is done with the slot)
                 if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));

@@ -106,8 +106,9 @@ struct PairScale {
 // columns, both reading the slot (two rows of opposite halves, or of opposite
 // parity for 64 dims) and writing the tile (rows of opposite parity).
 //
-// The loop over pieces is rolled on purpose: unrolled, the code of a tile runs
-// once a tile and comes from beyond the instruction caches every time.
+// What bounds the chunk kernel is the issue slots these instructions take from
+// the softmax (its time grows in step with the share of the slices converted),
+// so their number counts: an address is one xor, a scale one multiply-add.
 template <typename T, typename TC, int D, int BS>
 struct SliceConverter {
     static constexpr int ROWS = 32;
@@ -117,40 +118,38 @@ struct SliceConverter {
     static constexpr int NJ = D / 16;                   // pieces (rows) a lane takes
     static constexpr bool kRow = kRowScaled<TC>;
     using P = PairScale<T>;
+    static constexpr int kPairsUnrolled = 2;
     static_assert(D == 64 || D == 128, "head size");
     static_assert(BLOCKS * BS == ROWS && BS % NJ == 0, "a lane's rows lie in one block");
 
     int odd;            // piece j is row r0 + (j ^ odd) of the slice
     int r0;
-    uint32_t src, sca;  // the lane's codes and scale bytes, from the slot's start
-    uint32_t dst;       // its row r0 of the tile, from the tile's start
-    uint32_t ch;        // first of the piece's two 16-byte columns
+    uint32_t src;       // codes of row r0 from the slot's start
+    uint32_t sca;       // scale byte of row r0 from the slot's start
+    // First column of piece 0 from the slice's first row in the tile; its second
+    // column is at ^ 16, piece j at ^ (j * 128 | j * 16): the slice starts at a
+    // multiple of 1 KB, a row is 128 bytes, its 16-byte columns are permuted by
+    // the row's number mod 8.
+    uint32_t dst;
     Bf16Factors factors;
 
-    __device__ __forceinline__ SliceConverter(int w, int lane) {
+    __device__ __forceinline__ explicit SliceConverter(int lane) {
         odd = (lane >> 2) & 1;
         r0 = NJ * (D == 128 ? odd | ((lane >> 4) << 1) : lane >> 2);
         const int d = (lane & 3) * 16 + (D == 128 ? 64 * (((lane >> 3) & 1) ^ odd) : 0);
         src = (r0 / BS) * TILE + (r0 % BS) * D + d;
         sca = (r0 / BS) * TILE + BS * D + r0 % BS;
-        dst = (uint32_t)(d >> 6) * 16384u + (32 * w + r0) * 128;
-        ch = (d & 63) / 8;
+        const int r = r0 + odd;         // the row of piece 0
+        dst = (uint32_t)(d >> 6) * 16384u + r * 128 + (((uint32_t)(d & 63) / 8 ^ (r & 7)) << 4);
     }
 
-    __device__ __forceinline__ static int lds8(uint32_t addr) {
-        uint32_t v;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-        return (int)v;
+    __device__ __forceinline__ static void put(uint32_t at, const uint4& lo, const uint4& hi) {
+        sts128(at, lo);
+        sts128(at ^ 16u, hi);
     }
 
-    __device__ __forceinline__ void put(uint32_t tile, int u, const uint4& lo, const uint4& hi) const {
-        const uint32_t row = tile + dst + u * 128, t = (r0 + u) & 7;
-        sts128(row + ((ch ^ t) << 4), lo);
-        sts128(row + (((ch + 1) ^ t) << 4), hi);
-    }
-
-    // The slot at shared address `slot` into the tile at `tile`; rows at or past
-    // n, and rows of the blocks in `missing`, become zeros.
+    // The slot at shared address `slot` into a tile, its rows from address `tile`
+    // on; rows at or past n, and rows of the blocks in `missing`, become zeros.
     __device__ __forceinline__ void run(uint32_t slot, uint32_t tile, int n, uint32_t missing, int lane) const {
         bool plain = n >= ROWS && missing == 0;
         if constexpr (kRow) {
@@ -158,30 +157,35 @@ struct SliceConverter {
             const uint32_t far = (uint32_t)(lds8(slot + (lane / BS) * TILE + BS * D + lane % BS) - P::LO);
             plain = __all_sync(0xffffffffu, far <= (uint32_t)(P::HI - P::LO)) && plain;
         }
+        const uint32_t to = tile + dst;
         if (plain) {
-            uint4 a = lds128(slot + src + odd * D), b = lds128(slot + src + (1 ^ odd) * D);
-            int sa = 127, sb = 127;
+            // (rows of even and of odd pieces)
+            uint32_t even = slot + src + odd * D, other = slot + src + (1 ^ odd) * D;
+            uint4 a = lds128(even), b = lds128(other);
+            uint32_t sb[NJ / 4];        // the scale bytes, those of a pair in the order of its pieces
             if constexpr (kRow) {
-                sa = lds8(slot + sca + odd);
-                sb = lds8(slot + sca + (1 ^ odd));
+#pragma unroll
+                for (int k = 0; k < NJ / 4; ++k)
+                    sb[k] = __byte_perm((uint32_t)lds32(slot + sca + 4 * k), 0, odd ? 0x2301 : 0x3210);
             }
-#pragma unroll 1
+#pragma unroll kPairsUnrolled
             for (int j = 0; j < NJ; j += 2) {
                 const uint4 ca = a, cb = b;
-                const uint32_t ma = P::of(sa), mb = P::of(sb);
+                uint32_t ma = P::of(127), mb = ma;
+                if constexpr (kRow) {
+                    const uint32_t w = (NJ == 4 || j < 4 ? sb[0] : sb[NJ / 4 - 1]) >> (8 * (j & 2));
+                    ma = P::of((int)(w & 0xffu));
+                    mb = P::of((int)((w >> 8) & 0xffu));
+                }
                 if (j + 2 < NJ) {
-                    a = lds128(slot + src + ((j + 2) ^ odd) * D);
-                    b = lds128(slot + src + ((j + 3) ^ odd) * D);
-                    if constexpr (kRow) {
-                        sa = lds8(slot + sca + ((j + 2) ^ odd));
-                        sb = lds8(slot + sca + ((j + 3) ^ odd));
-                    }
+                    a = lds128(even + (j + 2) * D);
+                    b = lds128(other + (j + 2) * D);
                 }
                 uint4 lo, hi;
                 convert16<T, kRow>(ca, ma, factors, lo, hi);
-                put(tile, j ^ odd, lo, hi);
+                put(to ^ (uint32_t)(j * 144), lo, hi);
                 convert16<T, kRow>(cb, mb, factors, lo, hi);
-                put(tile, (j + 1) ^ odd, lo, hi);
+                put(to ^ (uint32_t)((j + 1) * 144), lo, hi);
             }
         } else {
 #pragma unroll 1
@@ -202,7 +206,7 @@ struct SliceConverter {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) *o[k] = P::kHalf ? mul_f16x2(*o[k], m2) : mul_bf16x2(*o[k], m2);
                 }
-                put(tile, u, lo, hi);
+                put(to ^ (uint32_t)(j * 144), lo, hi);
             }
         }
     }

@@ -30,8 +30,9 @@
 //                      a context's end in its last block;
 //   warp 11            takes items from the counter, hands them to the other
 //                      roles through a ring in shared memory, and loads q.
-//   warps 12-15, 16-19 E4M3 caches only, in place of warps 9 and 10: fetch the
-//                      codes of K and V and convert them (prefill_convert.cuh).
+//   warps 9, 10, 12-15 E4M3 caches only, in place of the TMA streams: fetch the
+//                      codes of K and V in slices of 32 rows and convert them
+//                      (prefill_convert.cuh).
 // Per key tile i of N = 128 keys and query tile x, in tensor memory
 // columns [256x, 256x + 256): S_x (128 fp32 columns), P_x over the first 64
 // of them (16-bit pairs), O_x (D fp32 columns) after S_x:
@@ -109,15 +110,17 @@ struct PrefillShape {
     static constexpr uint32_t KV_BYTES = DH * KV_HALF;      // K or V of one key tile
     static constexpr uint32_t OFF_K = 2 * Q_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + KST * KV_BYTES;
-    static constexpr uint32_t OFF_STG = OFF_V + VST * KV_BYTES;     // E4M3 caches: 4 warps x (K slot, V slot)
+    static constexpr uint32_t OFF_STG = OFF_V + VST * KV_BYTES;     // E4M3 caches: a slot for each converting warp
     static constexpr uint32_t STG_SLOT = kConvert ? 32 / BS * cache_tile_bytes<TC>(D, BS) : 0;
-    static constexpr uint32_t OFF_BAR = OFF_STG + 8 * STG_SLOT;
-    static constexpr uint32_t NBAR = 2 * IR + 4 + 2 * (KST + VST) + 10 + (kConvert ? 8 : 0);
+    static constexpr uint32_t OFF_BAR = OFF_STG + 6 * STG_SLOT;
+    static constexpr uint32_t NBAR = 2 * IR + 4 + 2 * (KST + VST) + 10 + (kConvert ? 6 : 0);
     static constexpr uint32_t OFF_ITEMS = (OFF_BAR + 8 * NBAR + 63) / 64 * 64;   // item ring, 64 bytes a slot
     static constexpr uint32_t OFF_HOLD = OFF_ITEMS + 64 * IR;                   // tensor-memory address
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;  // 1 KB alignment slack
-    static constexpr int kSoftmaxRegs = 136, kIssueRegs = 80, kConvertRegs = 64;
-    static_assert(2 * kSoftmaxRegs + kIssueRegs + 2 * kConvertRegs <= 5 * 96, "registers of the 640 threads at launch");
+    // E4M3 caches: warps that convert, and the registers of the softmax's two
+    // warpgroups and of the two others
+    static constexpr int kConvertWarps = 6, kSoftmaxRegs = 168, kSideRegs = 88;
+    static_assert(2 * kSoftmaxRegs + 2 * kSideRegs <= 4 * 128, "registers of the 512 threads at launch");
     static constexpr uint32_t TM_TILE = 256;                // columns per query tile
     static constexpr uint32_t TM_S = 0;                     // S (N fp32 columns); P over its first N/2
     static constexpr uint32_t TM_O = N;                     // O at columns N .. N + D
@@ -127,12 +130,13 @@ struct PrefillShape {
     static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM");
 };
 
-// An E4M3 cache takes two more warpgroups, whose warps convert the tiles (and
-// leaves the TMA warps 9 and 10 without work).  Its 640 threads start with 96
-// registers each, too few for the softmax's rows; the warpgroups share the
-// CTA's 5 * 96 a thread out again.
+// An E4M3 cache takes a fourth warpgroup; its four warps and two of the third
+// (the TMA warps of the other caches) convert the tiles.  Four warps bound the
+// kernel (bf16 chunks 940 us), eight on a fifth warpgroup left the softmax and
+// the MMA thread too few registers (812 us; the 16-bit kernel itself, built for
+// 640 threads, went from 655 to 755).
 template <typename T, typename TC>
-constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 640;
+constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 512;
 
 
 // One work item as the scheduler hands it to the other roles.
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     constexpr int N = S::N;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr bool kConvert = S::kConvert;
-    constexpr uint32_t kFullArrivals = kConvert ? 4 : 1;   // the converting warps, or the TMA thread
+    constexpr uint32_t kFullArrivals = kConvert ? 4 : 1;   // the slices of a tile, or the TMA thread
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_s = smem_addr(smem_raw);
     const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
@@ -187,11 +191,11 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
     auto bar_ofree = [&](int x) { return bar + 8 * (B0 + 6 + x); };  // O_x written out (128 arrivals)
     const uint32_t bar_vz = bar + 8 * (B0 + 8);
     const uint32_t bar_fin = bar + 8 * (B0 + 9);
-    auto bar_stg = [&](int w, int v) { return bar + 8 * (B0 + 10 + 2 * w + v); };   // E4M3: a staging slot filled
+    auto bar_stg = [&](int k) { return bar + 8 * (B0 + 10 + k); };   // E4M3: staging slot k filled
     PrefillItem* items = reinterpret_cast<PrefillItem*>(smem + S::OFF_ITEMS);
     uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + S::OFF_HOLD);
-    // warps 0-7, and warp 8 and the K/V producers (9 and 10, or 12-19) once each
-    constexpr int kItemReaders = kConvert ? 17 : 11;
+    // warps 0-7, and warp 8 and the K/V producers (9 and 10, or the converting warps) once each
+    constexpr int kItemReaders = kConvert ? 9 + S::kConvertWarps : 11;
     if (threadIdx.x == 0) {
         for (int k = 0; k < IR; ++k) {
             mbar_init(bar_ifull(k), 1);
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
         mbar_init(bar_vz, 1);
         mbar_init(bar_fin, 1);
         if constexpr (kConvert)
-            for (int k = 0; k < 8; ++k) mbar_init(bar_stg(k >> 1, k & 1), 1);
+            for (int k = 0; k < S::kConvertWarps; ++k) mbar_init(bar_stg(k), 1);
         fence_mbar_init();
     }
     if (threadIdx.x == 32) {
@@ -261,103 +265,8 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
         return true;
     };
 
-    if (kConvert && warp >= 12) {
-        // ===================== converting producers: warps 12-15 K, warps 16-19 V =====================
-        if constexpr (kConvert) {
-            reg_dec<S::kConvertRegs>();
-            using Slice = SliceConverter<T, TC, D, BS>;
-            constexpr int BPW = Slice::BLOCKS, TPE = 32 / BPW;   // blocks a slice; tiles a load of ids covers
-            static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
-            const int w = (warp - 12) & 3, v = (warp - 12) >> 2;   // slice, stream (0: K, 1: V)
-            const Slice conv(w, lane);
-            const uint32_t slot = sm + S::OFF_STG + (2 * w + v) * S::STG_SLOT, landed = bar_stg(w, v);
-            const unsigned char* cache = v ? p.v_cache : p.k_cache;
-            const int nst = v ? VST : KST;
-            bool ok = true;
-            int jt = 0;                          // key tiles converted
-            int copies = 0;                      // copies requested into the slot
-            // the tile whose copies are requested next
-            PrefillItem it;
-            int j = 0, t = 0, nT = 0, ids = -1;
-            int phys[BPW];
-            uint32_t missing = 0;
-            bool more = true;
-            auto begin_item = [&]() {
-                more = take_item(j, it);
-                if (!more) { ok = false; return; }
-                more = it.s >= 0;
-                t = 0;
-                nT = max(it.nT0, it.nT1);
-            };
-            // the blocks of tile t's slice; lane l holds the id of block l % BPW
-            // of the slice of tile l / BPW of a run of TPE tiles
-            auto find_blocks = [&]() {
-                const int nblk = (it.L + BS - 1) / BS;
-                if (t % TPE == 0) {
-                    const int lb = (t + lane / BPW) * S::BPT + w * BPW + lane % BPW;
-                    ids = -1;
-                    if (lb < nblk) {
-                        ids = __ldg(p.block_tables + (size_t)it.s * p.max_blocks_per_seq + lb);
-                        if (ids < 0 || ids >= p.num_blocks) {
-                            ids = -1;
-                            flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                        }
-                    }
-                }
-                missing = 0;
-#pragma unroll
-                for (int i = 0; i < BPW; ++i) {
-                    phys[i] = __shfl_sync(kAll, ids, (t % TPE) * BPW + i);
-                    if (phys[i] < 0) missing |= 1u << i;
-                }
-            };
-            auto request = [&]() {
-                if (lane == 0) {
-                    uint32_t n = 0;
-#pragma unroll
-                    for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
-                    mbar_arrive_expect_tx(landed, n);
-#pragma unroll
-                    for (int i = 0; i < BPW; ++i)
-                        if (phys[i] >= 0)
-                            bulk_g2s(slot + i * Slice::TILE, cache + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE,
-                                     Slice::TILE, landed);
-                }
-                ++copies;
-            };
-            begin_item();
-            if (more) {
-                find_blocks();
-                request();
-            }
-            for (; jt < copies; ++jt) {
-                const int st = jt % nst;
-                if (!warp_wait(landed, jt & 1, wl) ||
-                    (jt >= nst && !warp_wait(v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
-                    ok = false;
-                    break;
-                }
-                conv.run(slot, v ? v_base(st) : k_base(st), it.L - t * N - 32 * w, missing, lane);
-                fence_proxy_async();             // before the tensor core reads the tile
-                __syncwarp();                    // (and every lane is done with the slot)
-                if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));
-                // the slot's next tile, which may be the next item's first
-                if (++t == nT) {
-                    ++j;
-                    begin_item();
-                }
-                if (more) {
-                    find_blocks();
-                    request();
-                }
-            }
-            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
-            // the last copy lands before this warp leaves
-            if (copies > 0) mbar_wait_bounded(landed, (copies - 1) & 1, kWaitLimit);
-            __syncwarp();
-        }
-    } else if (warp >= 8) {
-        if constexpr (kConvert) reg_dec<S::kIssueRegs>();
+    if (warp >= 8) {
+        if constexpr (kConvert) reg_dec<S::kSideRegs>();
         if (warp == 11) {
             // ===================== scheduler: items from the counter, q by TMA =====================
             const int pairs = p.num_seqs * Hkv;
@@ -541,7 +450,112 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                 tc05::commit(bar_fin);
                 mbar_wait_bounded(bar_fin, 0, kWaitLimit);
             }
-        } else if constexpr (!kConvert) {
+        } else if constexpr (kConvert) {
+            // ============ converting producers: warps 9, 10 and 12-15, slices of K and V in turn ============
+            using Slice = SliceConverter<T, TC, D, BS>;
+            constexpr int BPW = Slice::BLOCKS, TPE = 32 / S::BPT;   // blocks a slice; tiles a load of ids covers
+            static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
+            const int cw = warp < 12 ? warp - 9 : warp - 10;     // of kConvertWarps
+            const Slice conv(lane);
+            const uint32_t slot = sm + S::OFF_STG + cw * S::STG_SLOT, landed = bar_stg(cw);
+            bool ok = true;
+            int copies = 0;                      // copies requested into the slot
+            // The slice whose copies are requested next: the k-th (K 0-3, V 0-3) of
+            // the jt-th tile of the CTA, tile t of item j.
+            PrefillItem it;
+            int j = 0, jt = 0, t = 0, nT = 0, k = cw;
+            int phys[BPW];
+            uint32_t missing = 0;
+            bool more = true;
+            auto begin_item = [&]() {
+                more = take_item(j, it);
+                if (!more) { ok = false; return; }
+                more = it.s >= 0;
+                t = 0;
+                nT = max(it.nT0, it.nT1);
+            };
+            // block ids of the item's tiles ids_t .. + TPE - 1 (lane l: the l-th
+            // block) and of the TPE tiles after them
+            int ids_t = 0, ids = -1, ids_next = -1;
+            auto load_ids = [&](int t0) -> int {
+                const int lb = t0 * S::BPT + lane;
+                int id = -1;
+                if (lb < (it.L + BS - 1) / BS) {
+                    id = __ldg(p.block_tables + (size_t)it.s * p.max_blocks_per_seq + lb);
+                    if (id < 0 || id >= p.num_blocks) {
+                        id = -1;
+                        flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                    }
+                }
+                return id;
+            };
+            auto request = [&]() {
+                const int w = k & 3;
+                if (t == ids_t + TPE) {
+                    ids_t = t;
+                    ids = ids_next;
+                    ids_next = load_ids(t + TPE);
+                }
+                missing = 0;
+#pragma unroll
+                for (int i = 0; i < BPW; ++i) {
+                    phys[i] = __shfl_sync(kAll, ids, (t - ids_t) * S::BPT + w * BPW + i);
+                    if (phys[i] < 0) missing |= 1u << i;
+                }
+                if (lane == 0) {
+                    uint32_t n = 0;
+#pragma unroll
+                    for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
+                    mbar_arrive_expect_tx(landed, n);
+                    const unsigned char* cache = k & 4 ? p.v_cache : p.k_cache;
+#pragma unroll
+                    for (int i = 0; i < BPW; ++i)
+                        if (phys[i] >= 0)
+                            bulk_g2s(slot + i * Slice::TILE, cache + ((size_t)phys[i] * Hkv + it.g) * Slice::TILE,
+                                     Slice::TILE, landed);
+                }
+                ++copies;
+            };
+            auto start_item = [&]() {
+                begin_item();
+                if (more) {
+                    ids_t = 0;
+                    ids = load_ids(0);
+                    ids_next = load_ids(TPE);
+                }
+            };
+            start_item();
+            if (more) request();
+            for (int n = 0; n < copies; ++n) {
+                const bool is_v = k & 4;
+                const int nst = is_v ? VST : KST, st = jt % nst;
+                if (!warp_wait(landed, n & 1, wl) ||
+                    (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
+                    ok = false;
+                    break;
+                }
+                const int w = k & 3;
+                conv.run(slot, (is_v ? v_base(st) : k_base(st)) + w * (32 * 128), it.L - t * N - 32 * w, missing, lane);
+                fence_proxy_async();             // before the tensor core reads the tile
+                __syncwarp();                    // (and every lane is done with the slot)
+                if (lane == 0) mbar_arrive(is_v ? bar_vfull(st) : bar_kfull(st));
+                // the warp's next slice, which may be of the next tile and the next item
+                k += S::kConvertWarps;
+                if (k >= 8) {
+                    k -= 8;
+                    ++jt;
+                    if (++t == nT) {
+                        ++j;
+                        start_item();
+                    }
+                }
+                if (more) request();
+            }
+            if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
+            // the last copy lands before this warp leaves
+            if (copies > 0) mbar_wait_bounded(landed, (copies - 1) & 1, kWaitLimit);
+            __syncwarp();
+        } else {
             // ===================== TMA producers: warp 9 K, warp 10 V =====================
             const bool is_v = warp == 10;
             const int nst = is_v ? VST : KST;
