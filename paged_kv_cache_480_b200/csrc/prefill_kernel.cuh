@@ -130,11 +130,12 @@ struct PrefillShape {
     static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM");
 };
 
-// An E4M3 cache takes a fourth warpgroup; its four warps and two of the third
-// (the TMA warps of the other caches) convert the tiles.  Four warps bound the
-// kernel (bf16 chunks 940 us), eight on a fifth warpgroup left the softmax and
-// the MMA thread too few registers (812 us; the 16-bit kernel itself, built for
-// 640 threads, went from 655 to 755).
+// An E4M3 cache takes a fourth warpgroup: its four warps and two of the third
+// (the TMA warps of the other caches) convert the tiles.  Of 512-token chunks
+// over 2K-8K contexts (64 heads over 8 KV heads, bf16) four converting warps
+// took 940 us, six 792, eight on a fifth warpgroup 812: 640 threads leave the
+// softmax and the MMA thread too few registers (the 16-bit kernel itself,
+// built that way, goes from 655 to 755 us).
 template <typename T, typename TC>
 constexpr uint32_t kPrefillThreads = std::is_same<T, TC>::value ? 384 : 512;
 
@@ -451,19 +452,27 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                 mbar_wait_bounded(bar_fin, 0, kWaitLimit);
             }
         } else if constexpr (kConvert) {
-            // ============ converting producers: warps 9, 10 and 12-15, slices of K and V in turn ============
+            // ============ converting producers: warps 9, 10, 12 K, warps 13-15 V ============
+            // Three warps take a stream's slices (four a tile) in turn, so each has
+            // one or two of every tile: it waits for every phase of its stages'
+            // empty barriers, as a wait by parity requires.
             using Slice = SliceConverter<T, TC, D, BS>;
             constexpr int BPW = Slice::BLOCKS, TPE = 32 / S::BPT;   // blocks a slice; tiles a load of ids covers
             static_assert(Slice::SLOT == S::STG_SLOT, "staging layout");
             const int cw = warp < 12 ? warp - 9 : warp - 10;     // of kConvertWarps
+            constexpr int kStreamWarps = S::kConvertWarps / 2;
+            static_assert(kStreamWarps <= 4, "a slice of every tile for every warp");
+            const bool is_v = cw >= kStreamWarps;
+            const unsigned char* cache = is_v ? p.v_cache : p.k_cache;
+            const int nst = is_v ? VST : KST;
             const Slice conv(lane);
             const uint32_t slot = sm + S::OFF_STG + cw * S::STG_SLOT, landed = bar_stg(cw);
             bool ok = true;
             int copies = 0;                      // copies requested into the slot
-            // The slice whose copies are requested next: the k-th (K 0-3, V 0-3) of
-            // the jt-th tile of the CTA, tile t of item j.
+            // The slice whose copies are requested next: the w-th of the jt-th tile of
+            // the CTA, tile t of item j.
             PrefillItem it;
-            int j = 0, jt = 0, t = 0, nT = 0, k = cw;
+            int j = 0, jt = 0, t = 0, nT = 0, w = cw % kStreamWarps;
             int phys[BPW];
             uint32_t missing = 0;
             bool more = true;
@@ -490,7 +499,6 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                 return id;
             };
             auto request = [&]() {
-                const int w = k & 3;
                 if (t == ids_t + TPE) {
                     ids_t = t;
                     ids = ids_next;
@@ -507,7 +515,6 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
 #pragma unroll
                     for (int i = 0; i < BPW; ++i) n += phys[i] >= 0 ? Slice::TILE : 0;
                     mbar_arrive_expect_tx(landed, n);
-                    const unsigned char* cache = k & 4 ? p.v_cache : p.k_cache;
 #pragma unroll
                     for (int i = 0; i < BPW; ++i)
                         if (phys[i] >= 0)
@@ -527,22 +534,20 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
             start_item();
             if (more) request();
             for (int n = 0; n < copies; ++n) {
-                const bool is_v = k & 4;
-                const int nst = is_v ? VST : KST, st = jt % nst;
+                const int st = jt % nst;
                 if (!warp_wait(landed, n & 1, wl) ||
                     (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl))) {
                     ok = false;
                     break;
                 }
-                const int w = k & 3;
                 conv.run(slot, (is_v ? v_base(st) : k_base(st)) + w * (32 * 128), it.L - t * N - 32 * w, missing, lane);
                 fence_proxy_async();             // before the tensor core reads the tile
                 __syncwarp();                    // (and every lane is done with the slot)
                 if (lane == 0) mbar_arrive(is_v ? bar_vfull(st) : bar_kfull(st));
                 // the warp's next slice, which may be of the next tile and the next item
-                k += S::kConvertWarps;
-                if (k >= 8) {
-                    k -= 8;
+                w += kStreamWarps;
+                if (w >= 4) {
+                    w -= 4;
                     ++jt;
                     if (++t == nT) {
                         ++j;
