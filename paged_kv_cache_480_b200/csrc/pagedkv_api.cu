@@ -246,7 +246,7 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     if (ps == 0) return PKV_ERR_INVALID_ARG;
     // Small groups over row caches: 192 tokens, or the 8 blocks that the
     // workspace is sized for (64 sequences of 256-2048 tokens, 40 heads: 128, 192
-    // and 256 tokens take 144, 142 and 148 us, the choice per call 151; the same
+    // and 256 tokens take 144, 142 and 147 us, the choice per call 147; the same
     // order for 4 to 256 sequences of up to 16K tokens and for 64 dims)
     if (kind == pkv::CacheKind::kFp8Row && partition_size == 0 && num_heads / num_kv_heads < 4)
         ps = ps_hi = block_size == 16 ? 192 : 8 * block_size;

@@ -12,6 +12,31 @@
 namespace pkv {
 namespace {
 
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t f2pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2unpack(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2sub(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 constexpr int kThreads = 64;        // about that many a CTA; twice that when a token is split
 constexpr int kMostThreads = 160;
 
@@ -64,38 +89,55 @@ struct Unit {
         Elem<T>::widen(r.a, x);
         Elem<T>::widen(r.b, x + E);
     }
+    __device__ __forceinline__ static Raw narrow(const float (&x)[2 * E]) {
+        return Raw{Elem<T>::narrow(x), Elem<T>::narrow(x + E)};
+    }
 
-    // Where a token's pair i keeps its cos and sin: the pairs of one unit lie
-    // `span` = ceil(rot / 2 / E) apart, so that neighbouring units read
-    // neighbouring words (together, a unit's pairs would put four lanes of
-    // every read on one bank).
-    __device__ __forceinline__ static int angle(int i, int span) { return i % E * span + i / E; }
+    // Where a token's pair i keeps cos (sin two floats further): pairs i and i + 1
+    // of a unit share four floats, and those of neighbouring units are
+    // neighbours (span = ceil(rot / 2 / E) units), so that the lanes of a read
+    // touch different banks.
+    __device__ __forceinline__ static int angle(int i, int span) {
+        return ((i % E) / 2 * span + i / E) * 4 + (i & 1);
+    }
 
-    __device__ __forceinline__ static void rotate(const float2* cs, int span, int u, int rot, float (&x)[2 * E]) {
+    // The unit's pairs by their angles, two at a time in packed fp32.
+    __device__ __forceinline__ static void rotate(const float4* cs, int span, int u, int rot, float (&x)[2 * E]) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            float& a = x[INTERLEAVED ? 2 * j : j];
-            float& b = x[INTERLEAVED ? 2 * j + 1 : E + j];
-            if (u * E + j < rot / 2) {
-                const float2 w = cs[j * span + u];
-                const float y = a * w.x - b * w.y;
-                b = b * w.x + a * w.y;
-                a = y;
+        for (int j = 0; j < E; j += 2) {
+            float& a0 = x[INTERLEAVED ? 2 * j : j];
+            float& b0 = x[INTERLEAVED ? 2 * j + 1 : E + j];
+            float& a1 = x[INTERLEAVED ? 2 * j + 2 : j + 1];
+            float& b1 = x[INTERLEAVED ? 2 * j + 3 : E + j + 1];
+            const float4 w = cs[j / 2 * span + u];
+            const uint64_t c = f2pack(w.x, w.y), s = f2pack(w.z, w.w), a = f2pack(a0, a1), b = f2pack(b0, b1);
+            const uint64_t ya = f2sub(f2mul(a, c), f2mul(b, s)), yb = f2fma(a, s, f2mul(b, c));
+            if (VEC && !INTERLEAVED) {              // whole units are rotated or none of it
+                f2unpack(ya, a0, a1);
+                f2unpack(yb, b0, b1);
+            } else {
+                float p0, p1, q0, q1;
+                f2unpack(ya, p0, p1);
+                f2unpack(yb, q0, q1);
+                if (u * E + j < rot / 2) { a0 = p0; b0 = q0; }
+                if (u * E + j + 1 < rot / 2) { a1 = p1; b1 = q1; }
             }
         }
     }
 
-    __device__ __forceinline__ static void store(T* row, int u, int rot, const float (&x)[2 * E]) {
+    __device__ __forceinline__ static void put(T* row, int u, int rot, const Raw& r) {
         if constexpr (VEC) {
             const int2 c = chunks(u, rot);
-            *reinterpret_cast<uint4*>(row + c.x) = Elem<T>::narrow(x);
-            *reinterpret_cast<uint4*>(row + c.y) = Elem<T>::narrow(x + E);
+            *reinterpret_cast<uint4*>(row + c.x) = r.a;
+            *reinterpret_cast<uint4*>(row + c.y) = r.b;
         } else {
+            const T* a = reinterpret_cast<const T*>(&r.a);
+            const T* b = reinterpret_cast<const T*>(&r.b);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 const int2 c = pair(u * E + j, rot);
-                row[c.x] = (T)x[j];
-                row[c.y] = (T)x[E + j];
+                row[c.x] = a[j];
+                row[c.y] = b[j];
             }
         }
     }
@@ -166,7 +208,7 @@ __global__ void __launch_bounds__(kMostThreads) rotary_kernel(const RotaryParams
     using UV = Unit<T, true, true>;        // rows that are not rotated: plain chunks
     constexpr int E = U::E;
     constexpr bool kCached = SINK != RowSink::kRows;
-    extern __shared__ float2 cs_all[];
+    extern __shared__ __align__(16) float angles[];
     __shared__ int64_t slots[kMaxTokens];
     griddep_wait();
     griddep_launch();
@@ -209,17 +251,24 @@ __global__ void __launch_bounds__(kMostThreads) rotary_kernel(const RotaryParams
         }
         return r;
     };
-    auto finish = [&](const Where& w, const typename U::Raw& raw) {
-        float x[2 * E];
-        U::widen(raw, x);
+    const float4* cs = reinterpret_cast<const float4*>(angles);
+    const int cs_token = span * E / 2;     // float4s of a token's angles
+    auto finish = [&](const Where& w, typename U::Raw raw) {
         const bool is_v = kCached && w.row >= H + Hkv;
+        const bool turned = w.t >= 0 && !is_v && w.u * E < half;
         const int64_t token = token0 + w.t;
-        if (w.t >= 0 && !is_v) U::rotate(cs_all + w.t * (span * E), span, w.u, p.rot, x);
+        float x[2 * E];
+        // (a unit that is neither rotated nor quantised goes on as it came)
+        if (SINK == RowSink::kCacheFp8Row || turned) {
+            U::widen(raw, x);
+            if (turned) U::rotate(cs + w.t * cs_token, span, w.u, p.rot, x);
+            if (SINK != RowSink::kCacheFp8Row || w.row < H) raw = U::narrow(x);
+        }
         if (w.t >= 0 && w.row < H)
-            U::store(static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)w.row * D, w.u, p.rot, x);
+            U::put(static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)w.row * D, w.u, p.rot, raw);
         if constexpr (!kCached) {
             if (w.t >= 0 && w.row >= H)
-                U::store(static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)(w.row - H) * D, w.u, p.rot, x);
+                U::put(static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)(w.row - H) * D, w.u, p.rot, raw);
         } else {
             const int g = w.row - H - (is_v ? Hkv : 0);
             int64_t slot = -1;
@@ -238,8 +287,8 @@ __global__ void __launch_bounds__(kMostThreads) rotary_kernel(const RotaryParams
             if constexpr (SINK == RowSink::kCache) {
                 if (put) {
                     T* dst = reinterpret_cast<T*>(cache) + ((blk * Hkv + g) * bs + off) * D;
-                    if (is_v) UV::store(dst, w.u, 0, x);
-                    else U::store(dst, w.u, p.rot, x);
+                    if (is_v) UV::put(dst, w.u, 0, typename UV::Raw{raw.a, raw.b});
+                    else U::put(dst, w.u, p.rot, raw);
                 }
             } else if (__any_sync(0xffffffffu, put)) {
                 // the row's largest magnitude over its D / (2 E) lanes
@@ -272,7 +321,10 @@ __global__ void __launch_bounds__(kMostThreads) rotary_kernel(const RotaryParams
     for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
         const int t = i / half;
         const int k = i - t * half;
-        cs_all[t * (span * E) + U::angle(k, span)] = turn(p.positions[token0 + t], p.inv_freq[k], p.mscale);
+        const float2 w = turn(p.positions[token0 + t], p.inv_freq[k], p.mscale);
+        float* at = angles + t * (span * E * 2) + U::angle(k, span);
+        at[0] = w.x;
+        at[2] = w.y;
     }
     __syncthreads();
     for (int base = first; base < last; base += step) {
