@@ -3,6 +3,7 @@
 // of whole sequences.  All are bound by HBM (each element is read and written
 // once) for many tokens and by latency for a few.
 #include <climits>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp8row.cuh"
@@ -401,20 +402,34 @@ cudaError_t by_sink(RotaryParams& p, RowSink sink, bool interleaved, int num_sms
 // Read-back: rows of the sequences' tokens from the pages to packed [N][Hkv][D].
 // A CTA takes a run of tokens; a thread finds each token's sequence (the last
 // one that starts at or before it) and block once, then the threads copy or
-// convert 16 cache bytes each, K and V.
+// convert 16 bytes of K and of V at a time.  The CTA's part of the output is
+// contiguous, so a unit's number is its place there.
 // ---------------------------------------------------------------------------
 constexpr int kGatherTokens = 32, kGatherThreads = 128;
+
+// The codes of 16 output bytes (4 for fp32, 8 for 16 bits), rounded once from the
+// exact product.
+template <typename T> struct CodeWord { using type = uint2; };
+template <> struct CodeWord<float> { using type = uint32_t; };
+__device__ __forceinline__ void widen_codes(uint32_t c, float* f) { Elem<fp8e4m3>::widen4(c, f); }
+__device__ __forceinline__ void widen_codes(const uint2& c, float* f) {
+    Elem<fp8e4m3>::widen4(c.x, f);
+    Elem<fp8e4m3>::widen4(c.y, f + 4);
+}
 
 template <typename T, CacheKind KIND>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
     constexpr int ES = KIND == CacheKind::kSame ? (int)sizeof(T) : 1;   // bytes of a cache element
-    constexpr int EPU = 16 / ES;                                        // elements of a unit
-    __shared__ int s_phys[kGatherTokens];   // physical block; -1: zeros (a bad id); -2: no row
-    __shared__ int s_off[kGatherTokens];
+    constexpr int EPU = Elem<T>::kPerChunk;                             // elements of a unit: 16 output bytes
+    using Word = typename std::conditional<KIND == CacheKind::kSame, uint4, typename CodeWord<T>::type>::type;
+    __shared__ int64_t s_base[kGatherTokens];   // row of KV head 0 in its cache; -1: zeros (a bad id); -2: no row
+    __shared__ int s_scale[kGatherTokens];      // its scale byte, from there
     griddep_wait();
     griddep_launch();
     const int64_t n0 = (int64_t)blockIdx.x * p.tokens_cta;
     const int tokens = (int)min((int64_t)p.tokens_cta, p.num_tokens - n0);
+    const int D = p.head_size, bs = 1 << p.block_shift;
+    const int tile = KIND == CacheKind::kFp8Row ? bs * (D + 1) : bs * D * ES;
     if ((int)threadIdx.x < tokens) {
         const int64_t n = n0 + threadIdx.x;
         int lo = 0, hi = p.num_seqs - 1;
@@ -423,50 +438,73 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
             if (p.start_loc[mid] <= n) lo = mid; else hi = mid - 1;
         }
         const int64_t t = n - p.start_loc[lo];
-        int phys = -2, off = 0;
+        int64_t base = -2;
+        const int off = (int)(t & (bs - 1));
         if (t >= 0 && n < p.start_loc[lo + 1]) {
             const int64_t j = t >> p.block_shift;
             if (j < p.max_blocks_per_seq) {
-                phys = p.block_tables[(int64_t)lo * p.max_blocks_per_seq + j];
-                off = (int)(t & ((1 << p.block_shift) - 1));
+                const int phys = p.block_tables[(int64_t)lo * p.max_blocks_per_seq + j];
                 if (phys < 0 || phys >= p.num_blocks) {
                     flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                    phys = -1;
+                    base = -1;
+                } else {
+                    base = (int64_t)phys * p.num_kv_heads * tile + off * D * ES;
                 }
             } else {
                 flag_error(p.errors, PKV_DEVERR_CONTEXT);
             }
         }
-        s_phys[threadIdx.x] = phys;
-        s_off[threadIdx.x] = off;
+        s_base[threadIdx.x] = base;
+        s_scale[threadIdx.x] = bs * D + off - off * D;
     }
     __syncthreads();
-    const int D = p.head_size, bs = 1 << p.block_shift;
-    const int upr = D / EPU, per_token = 2 * p.num_kv_heads * upr;
-    const int64_t tile = KIND == CacheKind::kFp8Row ? (int64_t)bs * (D + 1) : (int64_t)bs * D * ES;
-    for (int w = threadIdx.x; w < tokens * per_token; w += blockDim.x) {
-        const int i = w / per_token;
-        int rem = w - i * per_token;
-        const bool is_v = rem >= per_token / 2;
-        if (is_v) rem -= per_token / 2;
-        const int g = rem / upr, u = rem - g * upr;
-        const int phys = s_phys[i];
-        if (phys == -2) continue;
-        T* dst = static_cast<T*>(is_v ? p.v_out : p.k_out) + ((n0 + i) * p.num_kv_heads + g) * D + u * EPU;
-        uint4 c = make_uint4(0u, 0u, 0u, 0u);
-        const unsigned char* base = (is_v ? p.v_cache : p.k_cache) + ((int64_t)phys * p.num_kv_heads + g) * tile;
-        if (phys >= 0) c = *reinterpret_cast<const uint4*>(base + (s_off[i] * D + u * EPU) * ES);
-        if constexpr (KIND == CacheKind::kSame) {
-            *reinterpret_cast<uint4*>(dst) = c;
-        } else {
-            float f[16], sc = is_v ? p.v_scale : p.k_scale;
-            if constexpr (KIND == CacheKind::kFp8Row) sc = phys >= 0 ? row_scale(base[bs * D + s_off[i]]) : 0.f;
-            Elem<fp8e4m3>::widen(c, f);
-            constexpr int E = Elem<T>::kPerChunk;
+    const int upr = D / EPU, row_shift = 31 - __clz(upr);      // units of a row, a power of two
+    const int per_token = p.num_kv_heads * upr;
+    T* k_out = static_cast<T*>(p.k_out) + n0 * p.num_kv_heads * D;
+    T* v_out = static_cast<T*>(p.v_out) + n0 * p.num_kv_heads * D;
+    constexpr int kUnits = 4;                                  // in flight a thread
+    for (int w0 = threadIdx.x; w0 < tokens * per_token; w0 += kUnits * blockDim.x) {
+        Word ck[kUnits] = {}, cv[kUnits] = {};
+        int bk[kUnits], bv[kUnits];
+        bool on[kUnits];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] *= sc;
+        for (int k = 0; k < kUnits; ++k) {
+            const int w = w0 + k * blockDim.x;
+            bk[k] = bv[k] = 127;
+            on[k] = false;
+            if (w >= tokens * per_token) continue;
+            const int i = divide(w, p.token_inverse);
+            const int rem = w - i * per_token;
+            const int64_t base = s_base[i];
+            on[k] = base != -2;
+            if (base < 0) continue;
+            const int64_t at = base + (rem >> row_shift) * tile, codes = at + (rem & (upr - 1)) * (int)sizeof(Word);
+            ck[k] = *reinterpret_cast<const Word*>(p.k_cache + codes);
+            cv[k] = *reinterpret_cast<const Word*>(p.v_cache + codes);
+            if constexpr (KIND == CacheKind::kFp8Row) {
+                bk[k] = p.k_cache[at + s_scale[i]];
+                bv[k] = p.v_cache[at + s_scale[i]];
+            }
+        }
 #pragma unroll
-            for (int j = 0; j < 16 / E; ++j) reinterpret_cast<uint4*>(dst)[j] = Elem<T>::narrow(f + j * E);
+        for (int k = 0; k < kUnits; ++k) {
+            if (!on[k]) continue;
+            const int64_t to = (int64_t)(w0 + k * (int)blockDim.x) * EPU;
+            if constexpr (KIND == CacheKind::kSame) {
+                *reinterpret_cast<uint4*>(k_out + to) = ck[k];
+                *reinterpret_cast<uint4*>(v_out + to) = cv[k];
+            } else {
+                auto put = [&](T* dst, const Word& c, int b, float scale) {
+                    const float sc = KIND == CacheKind::kFp8Row ? row_scale(b) : scale;
+                    float f[EPU];
+                    widen_codes(c, f);
+#pragma unroll
+                    for (int j = 0; j < EPU; ++j) f[j] *= sc;
+                    *reinterpret_cast<uint4*>(dst) = Elem<T>::narrow(f);
+                };
+                put(k_out + to, ck[k], bk[k], p.k_scale);
+                put(v_out + to, cv[k], bv[k], p.v_scale);
+            }
         }
     }
 }
@@ -474,11 +512,12 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 template <typename T, CacheKind KIND>
 cudaError_t run_gather(GatherParams& p, int num_sms, cudaStream_t stream) {
     if (p.num_tokens == 0) return cudaSuccess;
-    // enough tokens for eight units a thread, fewer while the SMs are not filled
-    const int per_token = 2 * p.num_kv_heads * p.head_size / (KIND == CacheKind::kSame ? 16 / (int)sizeof(T) : 16);
-    int tpc = 8 * kGatherThreads / per_token;
+    // enough tokens for four units (K and V) a thread, fewer while the SMs are not filled
+    const int per_token = p.num_kv_heads * p.head_size / Elem<T>::kPerChunk;
+    int tpc = 4 * kGatherThreads / per_token;
     tpc = tpc < 1 ? 1 : tpc > kGatherTokens ? kGatherTokens : tpc;
     while (tpc > 1 && (p.num_tokens + tpc - 1) / tpc < 4 * num_sms) tpc >>= 1;
+    p.token_inverse = inverse_of(per_token);
     p.tokens_cta = tpc;
     const dim3 grid((unsigned)((p.num_tokens + tpc - 1) / tpc));
     return launch_pdl(gather_kernel<T, KIND>, grid, dim3(kGatherThreads), 0, stream, p);

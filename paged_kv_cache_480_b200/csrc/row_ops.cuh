@@ -49,7 +49,8 @@ struct GatherParams {
     unsigned int* errors;
     float k_scale, v_scale;
     int num_tokens, num_seqs, num_kv_heads, head_size, block_shift, num_blocks, max_blocks_per_seq;
-    int tokens_cta;            // filled by the launcher
+    int tokens_cta;            // filled by the launcher, as
+    uint32_t token_inverse;    // the inverse of a token's units
 };
 
 cudaError_t launch_gather(GatherParams p, CacheKind kind, int dtype, int num_sms, cudaStream_t stream);
