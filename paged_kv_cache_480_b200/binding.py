@@ -11,6 +11,7 @@ import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libpagedkv.so")
+FASTCALL_PATH = os.path.join(PKG, "_fastcall.so")
 
 PKV_OK = 0
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "CUDA error",
@@ -31,18 +32,19 @@ class OutOfBlocks(PagedKVError):
 
 
 _lib = None
+_fast = None            # _fastcall.so, bound to _lib
 _lock = threading.Lock()
 
 
 def load_library(path=LIB_PATH):
     """Open libpagedkv.so (once).  Raises if it has not been built."""
-    global _lib
+    global _lib, _fast
     with _lock:
         if _lib is not None:
             return _lib
-        if not os.path.exists(path):
-            raise FileNotFoundError(
-                f"{path} is missing: build it with `python -m paged_kv_cache_480_b200.build`")
+        for p in (path, FASTCALL_PATH):
+            if not os.path.exists(p):
+                raise FileNotFoundError(f"{p} is missing: build it with `python -m paged_kv_cache_480_b200.build`")
         lib = ctypes.CDLL(path)
         P, I, I64, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         lib.pkv_status_string.argtypes = [I]
@@ -125,7 +127,11 @@ def load_library(path=LIB_PATH):
         lib.pkv_bm_ref_count.restype = I
         lib.pkv_bm_utilisation.argtypes = [P]
         lib.pkv_bm_utilisation.restype = ctypes.c_double
-        _lib = lib
+        from . import _fastcall
+        for name in dir(_fastcall):
+            if name != "bind" and not name.startswith("_"):
+                _fastcall.bind(name, ctypes.cast(getattr(lib, name), P).value)
+        _lib, _fast = lib, _fastcall
         return lib
 
 
@@ -377,8 +383,8 @@ def fp8row_cache_shape(num_blocks, num_kv_heads, block_size, head_size):
 
 
 # The calls below are issued once a layer and step, often for a few tokens, when
-# the host's time counts: they pass plain integers, and read each tensor's
-# device as its index.
+# the host's time counts: they pass plain integers through _fastcall.so, and read
+# each tensor's device as its index.
 def _device(t, name):
     """Index of the GPU that t is on."""
     dev = t.get_device()
@@ -440,11 +446,12 @@ def _code(dtype):
 def _call(name, dev, stream, *args):
     """One library call on GPU dev, its stream last; raises on a bad status."""
     torch = _torch()
-    fn = getattr(_lib if _lib is not None else load_library(), name)
+    if _fast is None:
+        load_library()
     if torch._C._cuda_getDevice() != dev:       # launches go to the current device
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
-    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    st = getattr(_fast, name)(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if st != PKV_OK:
         _check(st, name)
 
@@ -514,7 +521,9 @@ def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, contex
         max_context_len = MB * bs
     code = _code(q.dtype)
     if workspace is None:
-        need = load_library().paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
+        if _fast is None:
+            load_library()
+        need = _fast.paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
         if need == 0:
             raise PagedKVError(2, "paged_attention_workspace_size")
         workspace = default_workspace(q.device, need)

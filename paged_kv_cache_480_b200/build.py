@@ -5,12 +5,15 @@ CUDA translation unit for ``-gencode arch=compute_100a,code=sm_100a`` in
 parallel and links them, with the host block manager, into
 ``paged_kv_cache_480_b200/libpagedkv.so`` (CUDA runtime linked statically).
 Objects go to ``paged_kv_cache_480_b200/_build/``; a unit is rebuilt when it
-or any header is newer than its object.
+or any header is newer than its object.  ``_fastcall.so`` beside it is a small
+CPython extension through which the binding makes the calls that are issued
+once a layer and step.
 """
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -76,6 +80,11 @@ def build(force=False, verbose=False, extra_nvcc=()):
         tmp = LIB + f".tmp{os.getpid()}"
         _run([_nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "py", "fastcall.cpp")
+    if force or _stale(src, FASTCALL, glob.glob(os.path.join(INCLUDE, "*.h"))):
+        tmp = FASTCALL + f".tmp{os.getpid()}"
+        _run(["g++"] + CXX_FLAGS + ["-I", sysconfig.get_paths()["include"], "-shared", "-o", tmp, src])
+        os.replace(tmp, FASTCALL)
     return LIB
 
 
