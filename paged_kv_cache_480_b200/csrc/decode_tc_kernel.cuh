@@ -123,7 +123,7 @@ struct DecodeTcShape {
 // (8-bit rows: two warpgroups convert; their tile rate is what bounds the kernel, so
 // the registers of 640 threads go round: 96 each at launch, shared out again.
 // Six converting warps of 512 threads, as in the prefill kernel, took 70 us for
-// 64 heads over one KV head against 62.)
+// 64 heads over one KV head against 57.)
 template <typename T, typename TC>
 constexpr uint32_t kDecodeTcThreads = std::is_same<T, TC>::value ? 352 : 640;
 

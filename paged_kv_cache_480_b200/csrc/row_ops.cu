@@ -38,8 +38,8 @@ __device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-constexpr int kThreads = 64;        // about that many a CTA; twice that when a token is split
-constexpr int kMostThreads = 160;
+constexpr int kThreads = 128;       // about that many a CTA (run_rotary); up to 32 more
+constexpr int kMostThreads = kThreads + 32;
 
 // Row lengths are multiples of 2 * kPerChunk elements, and a thread takes
 // kPerChunk pairs of one row: rotary pairs (2i, 2i + 1) or (i, i + rot / 2),
@@ -351,16 +351,20 @@ cudaError_t run_rotary(RotaryParams& p, bool interleaved, int num_sms, cudaStrea
     // A CTA takes whole tokens, enough of them for kDepth units a thread (at most
     // kMaxTokens: their angles stay within 16 KB); with too few such CTAs for the
     // SMs a token's units are split into parts of one unit a thread.
-    constexpr int kRound = kDepth * kThreads;
-    int tpc = kRound / p.units_token;
+    // About 128 threads a CTA, or 64 for many 16-bit tokens of the quantising write:
+    // 16384 of 32 + 32 heads take 121 us with 64 and 126 with 128, but the plain
+    // write 125 and 122, the same in 32 bits 209 and 207 (16384 of 8 + 1 heads of 64:
+    // 25 and 18), and 1500 tokens, whose CTAs are on the SMs all at once, 21 and 16.
+    int about = SINK == RowSink::kCacheFp8Row && sizeof(T) == 2 && p.num_tokens >= 16 * num_sms ? kThreads / 2
+                                                                                               : kThreads;
+    int tpc = kDepth * about / p.units_token;
     tpc = tpc < 1 ? 1 : tpc > kMaxTokens ? kMaxTokens : tpc;
     while (tpc > 1 && (p.num_tokens + tpc - 1) / tpc < 4 * num_sms) tpc >>= 1;
     const int groups = (p.num_tokens + tpc - 1) / tpc;
     p.tokens_cta = tpc;
     p.units_cta = p.units_token * tpc;
-    int parts = 1, depth = kDepth, about = kThreads;
+    int parts = 1, depth = kDepth;
     if (tpc == 1 && groups < 4 * num_sms) {
-        about = 2 * kThreads;
         const int most = (p.units_token + about - 1) / about;
         parts = (4 * num_sms + groups - 1) / groups;
         if (parts > most) parts = most;
@@ -368,9 +372,7 @@ cudaError_t run_rotary(RotaryParams& p, bool interleaved, int num_sms, cudaStrea
         parts = (p.units_token + p.units_cta - 1) / p.units_cta;
         depth = 1;
     }
-    // about 64 threads (chunks with the quantising write, 8192 tokens of 64 + 8
-    // heads: 63.9 us; 67.2 with 128 and 72 with 256), the count that leaves the
-    // fewest without a unit in the last round
+    // near that, the count that leaves the fewest without a unit in the last round
     int threads = about, idle = INT_MAX;
     for (int t = about + 32; t >= about - 32; t -= 32) {
         const int round = t * depth, over = (p.units_cta + round - 1) / round * round - p.units_cta;
