@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
             bk[k] = bv[k] = 127;
             on[k] = false;
             if (w >= tokens * per_token) continue;
-            const int i = divide(w, p.token_inverse);
+            const int i = tokens == 1 ? 0 : divide(w, p.token_inverse);   // (a row of many heads is past divide's range)
             const int rem = w - i * per_token;
             const int64_t base = s_base[i];
             on[k] = base != -2;

@@ -176,6 +176,35 @@ def test_gather_bad_pages_and_lengths():
     assert (k[:50] == 7).all() and torch.equal(k[50:66], c[3].transpose(0, 1)) and (k[82:] == 7).all()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_of_very_many_heads(dt):
+    """A token of more 16-byte units than 2^16."""
+    Hkv, D, bs, NB, dtype = 4099, 128, 16, 2, rm.DT[dt]
+    g = gen_of(3)
+    _, k, v = packed(g, 3, 1, Hkv, D, dtype)
+    slots = torch.tensor([17, 3, 16], device="cuda")
+    rows = [torch.zeros(pkv.fp8row_cache_shape(NB, Hkv, bs, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    same = [torch.zeros(NB, Hkv, bs, D, dtype=dtype, device="cuda") for _ in range(2)]
+    pkv.reshape_and_cache_fp8row(k, v, *rows, slots)
+    pkv.reshape_and_cache(k, v, *same, slots)
+    bt = torch.tensor([[1], [0]], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")    # slots 16, 17 and 0 to 3
+    at = torch.tensor([2, 0, 0, 0, 0, 1], device="cuda")                 # the tokens in them
+    some = torch.tensor([1, 1, 0, 0, 0, 1], device="cuda", dtype=dtype).view(6, 1, 1)
+    outs = lambda: [torch.full((6, Hkv, D), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    for o, x in zip(pkv.gather_cache(*outs(), *same, bt, start), (k, v)):
+        assert torch.equal(o, x[at] * some)
+    for o, c in zip(pkv.gather_cache_fp8row(*outs(), *rows, bt, start), rows):
+        cc, b = rm.codes_of(c, bs, D)
+        want = rm.value(cc, b)[[1, 1, 0, 0, 0, 0], :, [0, 1, 0, 1, 2, 3]].float().to(dtype)
+        assert torch.equal(o, want)
+    want = [torch.zeros_like(c) for c in rows]
+    for c, x in zip(want, (k, v)):
+        rm.put(c, bs, D, slots // bs, slots % bs, x)
+    assert torch.equal(rows[0], want[0]) and torch.equal(rows[1], want[1])
+    assert pkv.read_device_errors() == 0
+
+
 # ---- decode --------------------------------------------------------------------
 def paged_rows(lens, H, Hkv, D, bs, dt, seed, kscale=None, vscale=None):
     """q, dirty row caches holding the sequences' rows, and tables."""
