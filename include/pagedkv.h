@@ -260,9 +260,9 @@ pkv_status paged_attention_decode_fp8row(void* out, const void* q, const void* k
  * inv_freq[i],
  *   (x, y) -> attention_scale * (x cos a - y sin a, y cos a + x sin a),
  * a pair being elements (2i, 2i + 1) if interleaved, else (i, i + rotary_dim /
- * 2).  The other elements are copied.  Angles are formed and reduced in fp64,
- * the rotation is fp32 with one rounding at the end, so positions of any size
- * are as exact as near ones.
+ * 2).  The other elements are copied.  Angles are formed and reduced in fp64
+ * (at |p * inv_freq[i]| up to 2^31 they are off by less than 2^-20), the
+ * rotation is fp32 with one rounding at the end.
  *
  *   q_out, k_out   device, token t's head h at element t * *_token_stride + h *
  *                  head_size (written); may be q and k themselves with the

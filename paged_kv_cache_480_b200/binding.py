@@ -6,12 +6,13 @@ to the C ABI declared in ``include/pagedkv.h``.  All arithmetic runs in the
 library's CUDA kernels; if the library is missing, calls raise.
 """
 import ctypes
+import importlib.machinery
 import os
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libpagedkv.so")
-FASTCALL_PATH = os.path.join(PKG, "_fastcall.so")
+FASTCALL_PATH = os.path.join(PKG, "_fastcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 PKV_OK = 0
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "CUDA error",
@@ -32,7 +33,7 @@ class OutOfBlocks(PagedKVError):
 
 
 _lib = None
-_fast = None            # _fastcall.so, bound to _lib
+_fast = None            # the _fastcall extension, bound to _lib
 _lock = threading.Lock()
 
 
@@ -383,7 +384,7 @@ def fp8row_cache_shape(num_blocks, num_kv_heads, block_size, head_size):
 
 
 # The calls below are issued once a layer and step, often for a few tokens, when
-# the host's time counts: they pass plain integers through _fastcall.so, and read
+# the host's time counts: they pass plain integers through _fastcall, and read
 # each tensor's device as its index.
 def _device(t, name):
     """Index of the GPU that t is on."""

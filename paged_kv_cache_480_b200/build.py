@@ -5,11 +5,12 @@ CUDA translation unit for ``-gencode arch=compute_100a,code=sm_100a`` in
 parallel and links them, with the host block manager, into
 ``paged_kv_cache_480_b200/libpagedkv.so`` (CUDA runtime linked statically).
 Objects go to ``paged_kv_cache_480_b200/_build/``; a unit is rebuilt when it
-or any header is newer than its object.  ``_fastcall.so`` beside it is a small
+or any header is newer than its object.  ``_fastcall.*.so`` beside it is a small
 CPython extension through which the binding makes the calls that are issued
 once a layer and step.
 """
 import glob
+import importlib.machinery
 import os
 import subprocess
 import sys
@@ -22,7 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
-FASTCALL = os.path.join(PKG, "_fastcall.so")
+FASTCALL = os.path.join(PKG, "_fastcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,7 +1,7 @@
 // K and V tiles of the prefill kernel from an E4M3 cache: the tensor core takes
-// both operands of a product in q's 16-bit type, so four warps turn the codes
-// of each 128-key tile into that type on their way to shared memory, in the
-// 128-byte-swizzled layout that TMA gives the 16-bit caches.
+// both operands of a product in q's 16-bit type, so converting warps turn the
+// codes of each 128-key tile into that type on their way to shared memory, in
+// the 128-byte-swizzled layout that TMA gives the 16-bit caches.
 //
 // A code has four significant bits, so code * 2^e is exact in 16 bits but at
 // the ends of fp16's range.  The codes come through bulk copies, not loads
