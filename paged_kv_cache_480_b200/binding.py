@@ -172,15 +172,25 @@ def _contig(t, name):
 # workspace: one zero-initialised buffer per device, grown on demand
 # ---------------------------------------------------------------------------
 _workspaces = {}
+_outgrown = []          # (graphs that were captured with them may still be replayed)
 
 
 def default_workspace(device, nbytes):
-    """The binding's per-device workspace (not for concurrent streams)."""
+    """The binding's per-device workspace (not for concurrent streams).  It is
+    ready on every stream; a call that needs a larger one while its stream is
+    captured gets a workspace of the graph's own, zeroed at each replay."""
     import torch
     idx = device.index if device.index is not None else torch.cuda.current_device()
     ws = _workspaces.get(idx)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        with torch.cuda.device(idx):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            size = max(nbytes, 1 << 20, 0 if ws is None else 2 * ws.numel())
+            if ws is not None:
+                _outgrown.append(ws)
+            ws = torch.zeros(size, dtype=torch.uint8, device=device)
+            torch.cuda.current_stream().synchronize()
         _workspaces[idx] = ws
     return ws
 

@@ -8,6 +8,7 @@ import torch
 
 import paged_kv_cache_480_b200 as pkv
 import row_model as rm
+from paged_kv_cache_480_b200 import binding
 from test_gpu_rotary import gen_of, packed
 
 pytestmark = pytest.mark.gpu
@@ -668,4 +669,47 @@ def test_a_decode_step_captured_twice():
                 K, V = (rm.sequence(c, bs, D, bt, s, L) for c in (kc, vc))
                 ref, logit, top = rm.attend(b[3][s:s + 1], K, V, D ** -0.5)
                 rm.close(got[s:s + 1], ref, rm.attention_bound(ref, logit, top, torch.float16, torch.float16, L))
+    assert pkv.read_device_errors() == 0
+
+
+def test_the_bindings_workspace_in_graphs_and_on_streams(monkeypatch):
+    """Its first use inside a capture, its growth between a capture and the
+    replays, and its first use on a stream that is not the current one."""
+    monkeypatch.setattr(binding, "_workspaces", {})
+    H, Hkv, D, bs = 8, 2, 128, 16
+    lens = [700, 40, 1300]
+    kc, vc, bt, cl, gc = paged_rows(lens, H, Hkv, D, bs, "f16", 43)
+    q = torch.randn(3, H, D, generator=gc, device="cuda").half()
+    outs = torch.zeros(4, 3, H, D, dtype=torch.float16, device="cuda")
+
+    def step(out, **kw):
+        return pkv.paged_attention_decode_fp8row(out, q, kc, vc, bt, cl, D ** -0.5, **kw)
+    need = pkv.paged_attention_workspace_size(3, H, Hkv, D, bs, bt.shape[1] * bs, 1)
+    step(outs[0], workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    want = outs[0].clone()
+
+    def captured(out):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(out)
+        return graph
+    first = captured(outs[1])
+    assert binding._workspaces == {}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step(outs[2], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[2], want)
+    second = captured(outs[3])
+    old = binding._workspaces[q.device.index]
+    assert binding.default_workspace(q.device, old.numel() + 1).numel() == 2 * old.numel()
+    junk = torch.full((old.numel(),), 255, dtype=torch.uint8, device="cuda")    # what may lie in memory given back
+    for _ in range(3):
+        outs.zero_()
+        for graph in (first, second):
+            graph.replay()
+        step(outs[2])
+        assert all(torch.equal(o, want) for o in outs[1:])
+    del junk
     assert pkv.read_device_errors() == 0
