@@ -413,11 +413,13 @@ def _on(dev, t, name):
     return t.data_ptr()
 
 
-def _rows(dev, t, name):
-    """Device pointer of [T, heads, head_size] rows whose tokens may lie apart, and their stride."""
+def _rows(dev, t, shape, name):
+    """Device pointer of [T, heads, head_size] rows of this shape, whose tokens may lie apart, and their stride."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the GPU of the other tensors")
-    T, H, D = t.shape
+    T, H, D = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: heads must be contiguous within a token")
@@ -447,8 +449,7 @@ _DTYPE_CODES = {}
 
 
 def _code(dtype):
-    _torch()
-    code = _DTYPE_CODES.get(dtype)
+    code = _DTYPE_CODES.get(dtype)       # (filled by _torch())
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
     return code
@@ -472,16 +473,18 @@ def _row_caches(k_cache, v_cache, D):
     u8 = _torch().uint8
     if k_cache.dtype != u8 or v_cache.dtype != u8:
         raise TypeError("row caches are uint8 (fp8row_cache_shape)")
-    NB, Hkv, n = k_cache.shape
-    if v_cache.shape != k_cache.shape or n % (D + 1):
+    shape = k_cache.shape
+    NB, Hkv, n = shape
+    if v_cache.shape != shape or n % (D + 1):
         raise ValueError("row caches must be [num_blocks, num_kv_heads, block_size * (head_size + 1)]")
     return NB, Hkv, n // (D + 1)
 
 
 def _same_caches(k_cache, v_cache, D, dtype):
     """The same of a pair of caches that hold elements of one type."""
-    NB, Hkv, bs, D2 = k_cache.shape
-    if D2 != D or v_cache.shape != k_cache.shape or k_cache.dtype != dtype or v_cache.dtype != dtype:
+    shape = k_cache.shape
+    NB, Hkv, bs, D2 = shape
+    if D2 != D or v_cache.shape != shape or k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise ValueError("the caches must be [num_blocks, num_kv_heads, block_size, head_size] of the rows' dtype")
     return NB, Hkv, bs
 
@@ -502,15 +505,16 @@ def reshape_and_cache_fp8row(key, value, k_cache, v_cache, slot_mapping, stream=
     """Quantising cache write into 8-bit row caches (reshape_and_cache_fp8row in
     pagedkv.h): key/value [T, Hkv, D] in f32/f16/bf16, each (token, head) row
     with a scale of its own."""
-    T, Hkv, D = key.shape
+    shape, dtype = key.shape, key.dtype
+    T, Hkv, D = shape
     NB, Hkv2, bs = _row_caches(k_cache, v_cache, D)
-    if Hkv != Hkv2 or value.shape != key.shape or value.dtype != key.dtype:
+    if Hkv != Hkv2 or value.shape != shape or value.dtype != dtype:
         raise ValueError("key/value shape does not match the cache")
     dev = _device(key, "key")
-    kp, ks = _rows(dev, key, "key")
-    vp, vs = _rows(dev, value, "value")
+    kp, ks = _rows(dev, key, shape, "key")
+    vp, vs = _rows(dev, value, shape, "value")
     _call("reshape_and_cache_fp8row", dev, stream, kp, vp, _on(dev, k_cache, "k_cache"), _on(dev, v_cache, "v_cache"),
-          _int64(dev, slot_mapping, T, "slot_mapping"), T, Hkv, D, bs, NB, ks, vs, _code(key.dtype))
+          _int64(dev, slot_mapping, T, "slot_mapping"), T, Hkv, D, bs, NB, ks, vs, _code(dtype))
 
 
 def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len=None,
@@ -518,9 +522,10 @@ def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, contex
     """Decode attention over 8-bit row caches (paged_attention_decode_fp8row in
     pagedkv.h): q, out [S, H, D] in f32/f16/bf16; caches of fp8row_cache_shape."""
     int32 = _torch().int32
-    S, H, D = q.shape
+    shape, dtype = q.shape, q.dtype
+    S, H, D = shape
     NB, Hkv, bs = _row_caches(k_cache, v_cache, D)
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != shape or out.dtype != dtype:
         raise ValueError("out and q must share shape and dtype")
     if block_tables.dtype != int32 or context_lens.dtype != int32:
         raise TypeError("block_tables and context_lens must be int32")
@@ -530,7 +535,7 @@ def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, contex
     dev = _device(q, "q")
     if max_context_len is None:
         max_context_len = MB * bs
-    code = _code(q.dtype)
+    code = _code(dtype)
     if workspace is None:
         if _fast is None:
             load_library()
@@ -548,9 +553,10 @@ def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, contex
 def _prefill(name, caches, scales, out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
              max_query_len, stream):
     int32 = _torch().int32
-    T, H, D = q.shape
+    shape, dtype = q.shape, q.dtype
+    T, H, D = shape
     NB, Hkv, bs = caches
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != shape or out.dtype != dtype:
         raise ValueError("out and q must share shape and dtype")
     if block_tables.dtype != int32 or context_lens.dtype != int32 or query_start_loc.dtype != int32:
         raise TypeError("block_tables, context_lens and query_start_loc must be int32")
@@ -564,7 +570,7 @@ def _prefill(name, caches, scales, out, q, k_cache, v_cache, block_tables, conte
     _call(name, dev, stream, _on(dev, out, "out"), _on(dev, q, "q"), _on(dev, k_cache, "k_cache"),
           _on(dev, v_cache, "v_cache"), _on(dev, block_tables, "block_tables"),
           _on(dev, context_lens, "context_lens"), _on(dev, query_start_loc, "query_start_loc"), scale, *scales, T, S,
-          H, Hkv, D, bs, NB, MB, max_query_len, _code(q.dtype))
+          H, Hkv, D, bs, NB, MB, max_query_len, _code(dtype))
     return out
 
 
@@ -616,12 +622,14 @@ def _inv_freq(dev, t, D):
     return _on(dev, t, "inv_freq"), 2 * n
 
 
-def _rotated_pair(dev, o, x, T, D, dtype, name):
+def _rotated_pair(dev, o, x, shape, dtype, name):
     """(out pointer, out stride, in pointer, in stride) of rows and their rotated rows."""
-    if o.shape != x.shape or o.dtype != dtype or x.dtype != dtype or x.shape[0] != T or x.shape[2] != D:
+    if o.shape != shape or o.dtype != dtype or x.dtype != dtype:
         raise ValueError(f"{name} and {name}_out must be [T, heads, head_size] of q's dtype")
-    xp, xs = _rows(dev, x, name)
-    op, os = _rows(dev, o, name + "_out")
+    xp, xs = _rows(dev, x, shape, name)
+    if o is x:
+        return xp, xs, xp, xs
+    op, os = _rows(dev, o, shape, name + "_out")
     if op == xp and os != xs:
         raise ValueError(f"{name}_out in place of {name} must have its strides")
     return op, os, xp, xs
@@ -631,28 +639,36 @@ def rotary_embedding(q_out, k_out, q, k, positions, inv_freq, interleaved=False,
     """Rotary positions of q [T, H, D] and k [T, Hkv, D] (rotary_embedding in
     pagedkv.h).  q_out / k_out may be q / k; k and k_out may be None.
     positions: int64 [T]; inv_freq: float32 [rotary_dim / 2] on the device."""
-    T, H, D = q.shape
+    shape = q.shape
+    T, H, D = shape
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     dev, dtype = _device(q, "q"), q.dtype
-    qop, qos, qp, qs = _rotated_pair(dev, q_out, q, T, D, dtype, "q")
-    kop, kos, kp, ks = (None, 0, None, 0) if k is None else _rotated_pair(dev, k_out, k, T, D, dtype, "k")
+    qop, qos, qp, qs = _rotated_pair(dev, q_out, q, shape, dtype, "q")
+    Hkv, kop, kos, kp, ks = 0, None, 0, None, 0
+    if k is not None:
+        kshape = k.shape
+        T2, Hkv, D2 = kshape
+        if T2 != T or D2 != D:
+            raise ValueError("q and k must be [T, heads, head_size] of the same tokens and head size")
+        kop, kos, kp, ks = _rotated_pair(dev, k_out, k, kshape, dtype, "k")
     fp, rot = _inv_freq(dev, inv_freq, D)
-    _call("rotary_embedding", dev, stream, qop, kop, qp, kp, _int64(dev, positions, T, "positions"), fp, T, H,
-          0 if k is None else k.shape[1], D, rot, 1 if interleaved else 0, attention_scale, qos, kos, qs, ks,
-          _code(dtype))
+    _call("rotary_embedding", dev, stream, qop, kop, qp, kp, _int64(dev, positions, T, "positions"), fp, T, H, Hkv, D,
+          rot, 1 if interleaved else 0, attention_scale, qos, kos, qs, ks, _code(dtype))
 
 
 def _rotary_write(name, caches, q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
                   interleaved, attention_scale, stream):
     NB, Hkv, bs = caches
-    T, H, D = q.shape
+    shape = q.shape
+    T, H, D = shape
     dev, dtype = _device(q, "q"), q.dtype
-    if key.shape != (T, Hkv, D) or value.shape != key.shape or key.dtype != dtype or value.dtype != dtype:
+    kshape = (T, Hkv, D)
+    if key.shape != kshape or value.shape != kshape or key.dtype != dtype or value.dtype != dtype:
         raise ValueError("key and value must be [T, num_kv_heads, head_size] of q's dtype and match the caches")
-    qop, qos, qp, qs = _rotated_pair(dev, q_out, q, T, D, dtype, "q")
-    kp, ks = _rows(dev, key, "key")
-    vp, vs = _rows(dev, value, "value")
+    qop, qos, qp, qs = _rotated_pair(dev, q_out, q, shape, dtype, "q")
+    kp, ks = _rows(dev, key, kshape, "key")
+    vp, vs = _rows(dev, value, kshape, "value")
     fp, rot = _inv_freq(dev, inv_freq, D)
     _call(name, dev, stream, qop, qp, kp, vp, _on(dev, k_cache, "k_cache"), _on(dev, v_cache, "v_cache"),
           _int64(dev, positions, T, "positions"), _int64(dev, slot_mapping, T, "slot_mapping"), fp, T, H, Hkv, D, rot,
@@ -684,8 +700,9 @@ def rotary_reshape_and_cache_fp8row(q_out, q, key, value, k_cache, v_cache, posi
 def _gather(name, caches, scales, k_out, v_out, k_cache, v_cache, block_tables, start_loc, stream):
     int32 = _torch().int32
     NB, Hkv, bs = caches
-    T, Hkv2, D = k_out.shape
-    if Hkv2 != Hkv or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+    shape, dtype = k_out.shape, k_out.dtype
+    T, Hkv2, D = shape
+    if Hkv2 != Hkv or v_out.shape != shape or v_out.dtype != dtype:
         raise ValueError("k_out and v_out must be [T, num_kv_heads, head_size] and match the caches")
     if block_tables.dtype != int32 or start_loc.dtype != int32:
         raise TypeError("block_tables and start_loc must be int32")
@@ -695,7 +712,7 @@ def _gather(name, caches, scales, k_out, v_out, k_cache, v_cache, block_tables, 
     dev = _device(k_out, "k_out")
     _call(name, dev, stream, _on(dev, k_out, "k_out"), _on(dev, v_out, "v_out"), _on(dev, k_cache, "k_cache"),
           _on(dev, v_cache, "v_cache"), _on(dev, block_tables, "block_tables"), _on(dev, start_loc, "start_loc"),
-          *scales, T, S, Hkv, D, bs, NB, MB, _code(k_out.dtype))
+          *scales, T, S, Hkv, D, bs, NB, MB, _code(dtype))
     return k_out, v_out
 
 
