@@ -292,7 +292,16 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     }
 
     const int Greal = num_heads / num_kv_heads;
-    const int G = padded_group(Greal);              // kernel columns per item
+    int G = padded_group(Greal);                    // kernel columns per item
+    // fp32 q over row caches: the fp32 consumer's work bounds the call, and is the
+    // same for all slices of a group together, so a call with fewer items than
+    // warps takes narrower ones: 43 sequences of 237-403 tokens, 8 heads over one
+    // KV head, 34 us with 1 column and 162 with 8; but 300 of 500-4000 with 64 heads
+    // over 8, 2263 and 1371.  (The kernels of 1 and 2 columns take whole groups
+    // of that size only.)
+    if (kind == pkv::CacheKind::kFp8Row && dtype == PKV_F32)
+        while (G > 1 && (int64_t)num_seqs * wl.max_parts * num_kv_heads * ((Greal + G - 1) / G) < (int64_t)12 * sms)
+            G = G == 4 && Greal % 2 != 0 ? 1 : G / 2;
     const int slices = (Greal + G - 1) / G;
     // Shared memory: per-CTA lengths and prefix sums, then one ring per warp.
     const uint32_t seq_smem = (uint32_t)round_up(sizeof(int32_t) * (2 * (size_t)num_seqs + 1), 128);

@@ -274,6 +274,13 @@ def test_decode_many_short_sequences():
     check_decode([(7 * i) % 50 for i in range(500)], 4, 1, 64, 16, "bf16", seed=6)
 
 
+@pytest.mark.parametrize("S", [2, 60, 400])
+@pytest.mark.parametrize("G,D,bs", [(3, 128, 32), (6, 64, 32), (8, 128, 32), (8, 128, 16), (12, 64, 16)])
+def test_decode_f32_groups_whole_and_in_slices(S, G, D, bs):
+    """From calls that leave most warps idle to more items than warps."""
+    check_decode([(7 * i) % 70 for i in range(S)], 5 * G, 5, D, bs, "f32", seed=9)
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("G", [1, 8])
 def test_decode_rows_of_very_different_scales(dt, G):
