@@ -43,46 +43,42 @@ constexpr int kMostThreads = kThreads + 32;
 
 // Row lengths are multiples of 2 * kPerChunk elements, and a thread takes
 // kPerChunk pairs of one row: rotary pairs (2i, 2i + 1) or (i, i + rot / 2),
-// and beyond the rotated part neighbours.  Both 16-byte chunks of a unit are
-// loaded and stored whole (VEC) unless the half layout's offset rot / 2 is
-// not a whole number of chunks, when the unit's elements go one by one.  A
-// pair lives in one thread, so q_out may be q and k_out may be k.
-template <typename T, bool INTERLEAVED, bool VEC>
+// and beyond the rotated part neighbours.  A unit's elements are loaded and
+// stored in runs of W: whole 16-byte chunks unless the half layout's offset
+// rot / 2 is not a whole number of those, then as many elements as divide it
+// (12,968 tokens of 39 + 39 heads of 80, 40 rotated: 63 us with runs of 4, 358
+// one by one).  A pair lives in one thread, so q_out may be q and k_out may be k.
+template <int N> struct Run;
+template <> struct Run<1> { using type = unsigned char; };
+template <> struct Run<2> { using type = uint16_t; };
+template <> struct Run<4> { using type = uint32_t; };
+template <> struct Run<8> { using type = uint2; };
+template <> struct Run<16> { using type = uint4; };
+
+template <typename T, bool INTERLEAVED, int W>
 struct Unit {
     static constexpr int E = Elem<T>::kPerChunk;
+    using Elements = typename Run<W * sizeof(T)>::type;
+    using Codes = typename Run<W>::type;
+    static_assert(W <= E && (W == E || !INTERLEAVED), "runs of a unit");
 
-    // first elements of the unit's two chunks (VEC)
-    __device__ __forceinline__ static int2 chunks(int u, int rot) {
-        const int i0 = u * E;
-        if (!INTERLEAVED && i0 < rot / 2) return make_int2(i0, i0 + rot / 2);
-        return make_int2(2 * i0, 2 * i0 + E);
-    }
-    // element index of pair i's first and second element
-    __device__ __forceinline__ static int2 pair(int i, int rot) {
+    // First elements of the two runs that hold W pairs from pair i on.
+    __device__ __forceinline__ static int2 runs(int i, int rot) {
         if (!INTERLEAVED && i < rot / 2) return make_int2(i, i + rot / 2);
-        return make_int2(2 * i, 2 * i + 1);
+        return make_int2(2 * i, 2 * i + W);
     }
 
-    // A unit's elements as they are in memory: its two chunks, or (not VEC) its
-    // first and its second elements packed into two chunks.
+    // A unit's elements as they are in memory: the first and the second runs.
     struct Raw {
         uint4 a, b;
     };
     __device__ __forceinline__ static Raw fetch(const T* row, int u, int rot) {
         Raw x;
-        if constexpr (VEC) {
-            const int2 c = chunks(u, rot);
-            x.a = *reinterpret_cast<const uint4*>(row + c.x);
-            x.b = *reinterpret_cast<const uint4*>(row + c.y);
-        } else {
-            T* a = reinterpret_cast<T*>(&x.a);
-            T* b = reinterpret_cast<T*>(&x.b);
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int2 c = pair(u * E + j, rot);
-                a[j] = row[c.x];
-                b[j] = row[c.y];
-            }
+        for (int k = 0; k < E / W; ++k) {
+            const int2 c = runs(u * E + k * W, rot);
+            reinterpret_cast<Elements*>(&x.a)[k] = *reinterpret_cast<const Elements*>(row + c.x);
+            reinterpret_cast<Elements*>(&x.b)[k] = *reinterpret_cast<const Elements*>(row + c.y);
         }
         return x;
     }
@@ -113,7 +109,7 @@ struct Unit {
             const float4 w = cs[j / 2 * span + u];
             const uint64_t c = f2pack(w.x, w.y), s = f2pack(w.z, w.w), a = f2pack(a0, a1), b = f2pack(b0, b1);
             const uint64_t ya = f2sub(f2mul(a, c), f2mul(b, s)), yb = f2fma(a, s, f2mul(b, c));
-            if (VEC && !INTERLEAVED) {              // whole units are rotated or none of it
+            if (W == E && !INTERLEAVED) {           // whole units are rotated or none of it
                 f2unpack(ya, a0, a1);
                 f2unpack(yb, b0, b1);
             } else {
@@ -127,19 +123,11 @@ struct Unit {
     }
 
     __device__ __forceinline__ static void put(T* row, int u, int rot, const Raw& r) {
-        if constexpr (VEC) {
-            const int2 c = chunks(u, rot);
-            *reinterpret_cast<uint4*>(row + c.x) = r.a;
-            *reinterpret_cast<uint4*>(row + c.y) = r.b;
-        } else {
-            const T* a = reinterpret_cast<const T*>(&r.a);
-            const T* b = reinterpret_cast<const T*>(&r.b);
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int2 c = pair(u * E + j, rot);
-                row[c.x] = a[j];
-                row[c.y] = b[j];
-            }
+        for (int k = 0; k < E / W; ++k) {
+            const int2 c = runs(u * E + k * W, rot);
+            *reinterpret_cast<Elements*>(row + c.x) = reinterpret_cast<const Elements*>(&r.a)[k];
+            *reinterpret_cast<Elements*>(row + c.y) = reinterpret_cast<const Elements*>(&r.b)[k];
         }
     }
 
@@ -154,25 +142,14 @@ struct Unit {
     }
     __device__ __forceinline__ static void store_codes(unsigned char* row, int u, int rot, const float (&x)[2 * E],
                                                        float mult) {
-        uint32_t a[E / 4], b[E / 4];
+        __align__(8) uint32_t a[E / 4], b[E / 4];
         codes(x, mult, a);
         codes(x + E, mult, b);
-        if constexpr (VEC) {
-            const int2 c = chunks(u, rot);
-            if constexpr (E == 8) {
-                *reinterpret_cast<uint2*>(row + c.x) = make_uint2(a[0], a[1]);
-                *reinterpret_cast<uint2*>(row + c.y) = make_uint2(b[0], b[1]);
-            } else {
-                *reinterpret_cast<uint32_t*>(row + c.x) = a[0];
-                *reinterpret_cast<uint32_t*>(row + c.y) = b[0];
-            }
-        } else {
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int2 c = pair(u * E + j, rot);
-                row[c.x] = (unsigned char)(a[j / 4] >> (8 * (j % 4)));
-                row[c.y] = (unsigned char)(b[j / 4] >> (8 * (j % 4)));
-            }
+        for (int k = 0; k < E / W; ++k) {
+            const int2 c = runs(u * E + k * W, rot);
+            *reinterpret_cast<Codes*>(row + c.x) = reinterpret_cast<const Codes*>(a)[k];
+            *reinterpret_cast<Codes*>(row + c.y) = reinterpret_cast<const Codes*>(b)[k];
         }
     }
 };
@@ -203,10 +180,10 @@ __device__ __forceinline__ float2 turn(int64_t position, float inv_freq, float m
 constexpr int kDepth = 2;
 constexpr int kMaxTokens = 8;   // of a CTA
 
-template <typename T, RowSink SINK, bool INTERLEAVED, bool VEC>
+template <typename T, RowSink SINK, bool INTERLEAVED, int W>
 __global__ void __launch_bounds__(kMostThreads) rotary_kernel(const RotaryParams p) {
-    using U = Unit<T, INTERLEAVED, VEC>;
-    using UV = Unit<T, true, true>;        // rows that are not rotated: plain chunks
+    using U = Unit<T, INTERLEAVED, W>;
+    using UV = Unit<T, true, U::E>;        // rows that are not rotated: plain chunks
     constexpr int E = U::E;
     constexpr bool kCached = SINK != RowSink::kRows;
     extern __shared__ __align__(16) float angles[];
@@ -386,9 +363,12 @@ cudaError_t run_rotary(RotaryParams& p, bool interleaved, int num_sms, cudaStrea
     p.token_inverse = inverse_of(p.units_token);
     const size_t smem = sizeof(float2) * (size_t)tpc * ((p.rot / 2 + E - 1) / E * E);
     const dim3 grid((unsigned)groups, (unsigned)parts), block((unsigned)threads);
-    if (interleaved) return launch_pdl(rotary_kernel<T, SINK, true, true>, grid, block, smem, stream, p);
-    if ((p.rot / 2) % E == 0) return launch_pdl(rotary_kernel<T, SINK, false, true>, grid, block, smem, stream, p);
-    return launch_pdl(rotary_kernel<T, SINK, false, false>, grid, block, smem, stream, p);
+    const int half = p.rot / 2;
+    if (interleaved) return launch_pdl(rotary_kernel<T, SINK, true, E>, grid, block, smem, stream, p);
+    if (half % E == 0) return launch_pdl(rotary_kernel<T, SINK, false, E>, grid, block, smem, stream, p);
+    if (E == 8 && half % 4 == 0) return launch_pdl(rotary_kernel<T, SINK, false, 4>, grid, block, smem, stream, p);
+    if (half % 2 == 0) return launch_pdl(rotary_kernel<T, SINK, false, 2>, grid, block, smem, stream, p);
+    return launch_pdl(rotary_kernel<T, SINK, false, 1>, grid, block, smem, stream, p);
 }
 
 template <typename T>

@@ -34,7 +34,8 @@ def check(y, x, pos, f, il, att=1.0):
 
 CASES = [("f16", 1, 1, 1, 64, 64), ("f16", 3, 8, 2, 128, 128), ("bf16", 257, 32, 8, 128, 64), ("f32", 65, 5, 5, 64, 64),
          ("bf16", 700, 1, 1, 64, 32), ("f32", 9, 4, 1, 128, 20), ("f16", 33, 7, 7, 80, 32), ("bf16", 5, 3, 1, 128, 2),
-         ("f16", 17, 2, 2, 256, 66), ("f32", 4, 2, 1, 512, 512), ("bf16", 2, 96, 8, 16, 14), ("f16", 4096, 2, 1, 64, 64)]
+         ("f16", 17, 2, 2, 256, 66), ("f32", 4, 2, 1, 512, 512), ("bf16", 2, 96, 8, 16, 14), ("f16", 4096, 2, 1, 64, 64),
+         ("bf16", 300, 9, 3, 80, 40), ("f16", 21, 3, 1, 64, 24), ("bf16", 12, 2, 2, 128, 20), ("f32", 30, 3, 2, 64, 12)]
 
 
 @pytest.mark.parametrize("il", [False, True])
@@ -121,7 +122,8 @@ def test_rotary_captured_and_on_another_stream():
 
 @pytest.mark.parametrize("dt,T,H,Hkv,D,R,bs,il", [("bf16", 37, 8, 2, 128, 128, 16, False), ("f16", 5, 4, 4, 64, 32, 32, True),
                                                   ("f32", 300, 3, 1, 64, 20, 16, False), ("bf16", 1, 0, 3, 128, 64, 32, False),
-                                                  ("f32", 70, 2, 2, 128, 128, 16, True), ("bf16", 9, 2, 1, 64, 22, 16, False)])
+                                                  ("f32", 70, 2, 2, 128, 128, 16, True), ("bf16", 9, 2, 1, 64, 22, 16, False),
+                                                  ("f16", 19, 2, 3, 64, 24, 16, False), ("bf16", 19, 2, 3, 128, 20, 32, False)])
 def test_rotary_write_is_rotary_then_write(dt, T, H, Hkv, D, R, bs, il):
     """rotary_reshape_and_cache gives the bits of rotary_embedding followed by
     reshape_and_cache, and skips tokens without a slot."""

@@ -79,7 +79,8 @@ def test_write_of_special_rows():
 @pytest.mark.parametrize("dt,T,H,Hkv,D,R,bs,il", [("bf16", 260, 8, 8, 128, 128, 16, False), ("f16", 33, 16, 2, 128, 64, 32, True),
                                                   ("f32", 4, 4, 4, 64, 64, 16, False), ("f32", 50, 0, 3, 128, 20, 16, False),
                                                   ("bf16", 1, 5, 1, 64, 6, 32, False), ("f16", 1030, 1, 1, 64, 64, 16, False),
-                                                  ("f32", 21, 2, 1, 128, 126, 32, True)])
+                                                  ("f32", 21, 2, 1, 128, 126, 32, True), ("bf16", 30, 4, 2, 64, 40, 16, False),
+                                                  ("f16", 30, 3, 2, 128, 20, 32, False)])
 def test_rotary_write(dt, T, H, Hkv, D, R, bs, il):
     g = gen_of(T + R)
     q, k, v = packed(g, T, H, Hkv, D, rm.DT[dt], extra=16)
