@@ -368,7 +368,7 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     p.seq_smem = seq_smem;
 
     const size_t max_items = (size_t)num_seqs * wl.max_parts * num_kv_heads * slices;
-    size_t ctas = (max_items + W - 1) / W;
+    size_t ctas = kind == pkv::CacheKind::kFp8Row ? max_items : (max_items + W - 1) / W;
     if (ctas > (size_t)sms) ctas = sms;
     const size_t smem = seq_smem + (size_t)W * per_warp;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
