@@ -143,6 +143,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// A running maximum before the first key: finite, so that keys whose logits are
+// -inf weigh 2^(-inf) = 0 against it and those whose logits are NaN (which a
+// maximum passes over) make the weights, and so the sum l, NaN.  A partial
+// result without any weight has l = 0, and only those does the merge leave out.
+constexpr float kNoMax = -0x1p127f;
+
 // ===========================================================================
 // fp32 CUDA-core consumer.
 // lane = (token slot u, head h, dim group c); Q lanes share a token row, each
@@ -176,7 +182,7 @@ struct FmaConsumer {
         c = lane % Q;
         h = (lane / Q) % G;
         u = lane / (Q * G);
-        m_run = -INFINITY;
+        m_run = kNoMax;
         l_run = 0.f;
 #pragma unroll
         for (int d = 0; d < DL; ++d) qf[d] = acc[d] = 0.f;
@@ -201,7 +207,7 @@ struct FmaConsumer {
             }
 #pragma unroll
         for (int d = 0; d < DL; ++d) acc[d] = 0.f;
-        m_run = -INFINITY;
+        m_run = kNoMax;
         l_run = 0.f;
     }
 
@@ -254,7 +260,7 @@ struct FmaConsumer {
         for (int i = 1; i < PSTEP; ++i) mb = fmaxf(mb, z[i]);
 #pragma unroll
         for (int off = Q * G; off < 32; off <<= 1) mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, off));
-        const float m_new = fmaxf(m_run, mb);   // finite: nvalid > 0
+        const float m_new = fmaxf(m_run, mb);
         const float alpha = ex2(m_run - m_new);
         l_run *= alpha;
 #pragma unroll
@@ -383,7 +389,7 @@ struct MmaConsumer {
     __device__ __forceinline__ void init(int lane) {
         r = lane >> 2;
         c = lane & 3;
-        m0 = m1 = -INFINITY;
+        m0 = m1 = kNoMax;
         l0 = l1 = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -404,7 +410,7 @@ struct MmaConsumer {
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
-        m0 = m1 = -INFINITY;
+        m0 = m1 = kNoMax;
         l0 = l1 = 0.f;
     }
 
@@ -433,7 +439,7 @@ struct MmaConsumer {
             mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
             mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
         }
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);   // finite: nvalid > 0
+        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
         const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);
         m0 = n0;
         m1 = n1;
@@ -600,7 +606,7 @@ struct MmaConsumerFp8 {
     __device__ __forceinline__ void init(int lane) {
         r = lane >> 2;
         c = lane & 3;
-        m0 = m1 = -INFINITY;
+        m0 = m1 = kNoMax;
         l0 = l1 = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -625,7 +631,7 @@ struct MmaConsumerFp8 {
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
-        m0 = m1 = -INFINITY;
+        m0 = m1 = kNoMax;
         l0 = l1 = 0.f;
     }
 

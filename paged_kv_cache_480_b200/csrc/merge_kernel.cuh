@@ -3,8 +3,9 @@
 // unnormalised accumulator acc_p, the running max m_p (log2 units) and the
 // sum l_p, the exact identity
 //   M = max_p m_p,  w_p = 2^(m_p - M),  out = sum_p w_p acc_p / sum_p w_p l_p
-// gives the attention over the whole context.  Partials with m_p = -inf
-// (no key) are skipped.
+// gives the attention over the whole context.  Partials with l_p = 0 (no key
+// of any weight) are skipped.  One of NaN logits alone has l_p = NaN and no
+// maximum (m_p = -inf, or the lowest there is): it is not, and makes out NaN.
 //
 // Two layouts of the partials.  The CUDA-core decode numbers them through
 // per-sequence prefix sums it publishes (a sequence with one partition wrote
@@ -105,20 +106,20 @@ __global__ void __launch_bounds__(128) lse_merge_kernel(const ReduceParams p) {
     }
     __syncthreads();
     float M = -INFINITY, den = 0.f;
-    for (int q = 0; q < np; ++q) M = fmaxf(M, s_ml[q].x);
-    if (M != -INFINITY)
-        for (int q = 0; q < np; ++q)
-            if (s_ml[q].x != -INFINITY) den = fmaf(merge_ex2(s_ml[q].x - M), s_ml[q].y, den);
+    for (int q = 0; q < np; ++q)
+        if (s_ml[q].y != 0.f) M = fmaxf(M, s_ml[q].x);
+    for (int q = 0; q < np; ++q)
+        if (s_ml[q].y != 0.f) den = fmaf(merge_ex2(s_ml[q].x - M), s_ml[q].y, den);
 
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
+    if (den != 0.f) {
         for (int q0 = pg; q0 < np; q0 += 4 * NPG) {
             float4 a[4];
             float w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int q = q0 + k * NPG;
-                const bool ok = q < np && s_ml[q < np ? q : 0].x != -INFINITY;
+                const bool ok = q < np && s_ml[q < np ? q : 0].y != 0.f;
                 w[k] = ok ? merge_ex2(s_ml[q].x - M) : 0.f;
                 const float4 v = q0 == pg ? a0[k] : (ok ? acc[first + (size_t)q * stride] : make_float4(0.f, 0.f, 0.f, 0.f));
                 a[k] = ok ? v : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(128) lse_merge_kernel(const ReduceParams p) {
         num.z += v.z;
         num.w += v.w;
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den != 0.f ? 1.f / den : 0.f;     // (NaN stays NaN)
     const float f[4] = {num.x * inv, num.y * inv, num.z * inv, num.w * inv};
     T* o = reinterpret_cast<T*>(p.out) + ((size_t)s * p.num_heads + h) * D + d4 * 4;
 #pragma unroll
