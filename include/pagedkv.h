@@ -97,7 +97,8 @@ const char* pkv_version(void);
  *                  ceil(context_len / block_size) are never read
  *   context_lens   device, int32 [num_seqs]; tokens to attend (includes the
  *                  step's own token once reshape_and_cache wrote it)
- *   scale          softmax scale (usually 1/sqrt(head_size))
+ *   scale          softmax scale (usually 1/sqrt(head_size)), of either sign or
+ *                  0; NaN is refused (PKV_ERR_INVALID_ARG)
  *   num_kv_heads   KV heads; num_heads must be a multiple (G = num_heads /
  *                  num_kv_heads, any value: MHA, GQA and MQA)
  *   block_size     tokens per block, 16 or 32
@@ -124,7 +125,7 @@ const char* pkv_version(void);
  *
  * Supported: dtype f32/f16/bf16, head_size 64 or 128, block_size 16 or 32,
  * any G, num_seqs <= 16384.  Anything else: PKV_ERR_UNSUPPORTED.  With f16
- * or bf16 elements, G >= 16 and partition_size 0, the call runs on the
+ * or bf16 elements, G >= 16, scale > 0 and partition_size 0, the call runs on the
  * tcgen05 tensor cores: the rows of each product are the group's query heads
  * (slices of up to 128), and the key tiles of all (sequence, KV head, slice)
  * units are split into ranges of equal cost over one CTA per SM, whose
@@ -232,7 +233,7 @@ pkv_status reshape_and_cache_fp8kv(const void* key, const void* value, void* k_c
  * softmax weights are taken relative to the largest weight times V scale, so
  * rows of very different scales keep their precision.  With 16-bit q the
  * products run on the tensor cores in fp16 (bf16 q is rounded to fp16 there,
- * so |q| must stay below 65504).  With 16-bit q, G >= 17 and partition_size 0
+ * so |q| must stay below 65504).  With 16-bit q, G >= 17, scale > 0 and partition_size 0
  * the call takes the tcgen05 kernel, in q's type: weights are rounded to it,
  * and elements are taken in it as in paged_attention_prefill_fp8row.
  * Workspace, partitioning, checks and errors as for paged_attention_decode.

@@ -111,12 +111,17 @@ struct WorkspaceLayout {
 // Whether a plain decode call takes the tensor-core split-context kernel:
 // 16-bit q, 16-bit or 8-bit row caches, at least kDecodeTcMinGroup (row caches:
 // kDecodeTcMinGroupRows) query heads per KV head, and the library's choice of
-// partitions.
+// partitions.  (A call whose scale that kernel's softmax cannot take goes to the
+// other one in a workspace of this size: tc_scale.)
 bool use_decode_tc(int num_heads, int num_kv_heads, int dtype, int partition_size,
                    pkv::CacheKind kind = pkv::CacheKind::kSame) {
     const int least = kind == pkv::CacheKind::kFp8Row ? pkv::kDecodeTcMinGroupRows : pkv::kDecodeTcMinGroup;
     return kind != pkv::CacheKind::kFp8 && dtype != PKV_F32 && num_heads / num_kv_heads >= least && partition_size == 0;
 }
+
+// The tensor-core kernel's softmax takes maxima of the logits before their scale
+// and hides keys by -inf: the scale has to be positive and finite in log2 units.
+bool tc_scale(float scale) { return scale > 0.f && scale * 1.4426950408889634f < INFINITY; }
 
 WorkspaceLayout workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                  int max_context_len, int ps, bool tc = false) {
@@ -253,7 +258,7 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     // over an FP8 cache the warps retire blocks twice as fast, so longer
     // partitions leave too few items per warp: at most 32 blocks there
     if (fp8_cache && ps_hi > 32 * block_size) ps_hi = 32 * block_size;
-    const bool tc = app == nullptr && use_decode_tc(num_heads, num_kv_heads, dtype, partition_size, kind);
+    const bool tc = app == nullptr && tc_scale(scale) && use_decode_tc(num_heads, num_kv_heads, dtype, partition_size, kind);
     const WorkspaceLayout wl =
         workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, ps, tc);
     if (!workspace || !aligned16(workspace) || workspace_bytes < wl.total) return PKV_ERR_WORKSPACE;
