@@ -539,6 +539,9 @@ pkv_status swap_blocks(const void* const* src_caches, void* const* dst_caches, i
  * block_size or queries outside [0, num_tokens) set PKV_DEVERR_CONTEXT and
  * the sequence's rows are not written; a block id outside the pool sets
  * PKV_DEVERR_BLOCK_ID and reads as zeros.
+ * A NaN or infinite element of V also reaches queries before its token, in its
+ * dim, if they share its 128 keys (128 i .. 128 i + 127 of the sequence): it is
+ * multiplied with their weight of 0.
  * Supported: head_size 64 or 128, block_size 16 or 32, G = num_heads /
  * num_kv_heads from 1 to 128 (a query tile of 128 rows holds floor(128 / G)
  * queries of G heads), num_blocks * num_kv_heads * block_size < 2^31.
@@ -557,7 +560,10 @@ pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache
  * cache: every argument, check and error as there, the caches as described
  * with those formats.  Each cache element is taken in q's type: exact in bf16
  * and within fp16's range; with f16 q an element of a row cache beyond +-65504
- * becomes infinity and one below 2^-24 rounds to a multiple of 2^-24. */
+ * becomes infinity (an f16 element from 63488 on is such a one: it was stored as
+ * 65536) and one below 2^-21 may be rounded, to a multiple of 2^-24.  Here NaN
+ * and infinite elements reach the queries that see their token and no others:
+ * an infinity of V makes its dim of the output infinite, both signs NaN. */
 pkv_status paged_attention_prefill_fp8kv(void* out, const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables, const int32_t* context_lens,
                                          const int32_t* query_start_loc, float scale, float k_scale, float v_scale,

@@ -73,13 +73,15 @@ __device__ __forceinline__ void convert16(const uint4& c, uint32_t m, const Bf16
 
 // Pair multipliers of scale bytes: one multiply-add for the exponents whose
 // multiplier is a normal number of the type, fp16: -14 .. 15, bf16: up to 7
-// (down to the -60 of the format).  A slice with any other byte takes
-// scale_up, two products: the first exact (down: codes are multiples of 2^-9,
+// (down to the -60 of the format).  For any other byte two products: the first
+// exact (down: codes are multiples of 2^-9,
 // times 2^-12 still of 2^-21) or an overflow (up).
 template <typename T>
 struct PairScale {
     static constexpr bool kHalf = std::is_same<T, __half>::value;
     static constexpr int LO = kHalf ? 127 - 14 : 1, HI = kHalf ? 127 + 15 : 127 + 7;
+    // up to it no element overflows (448 * 2^7 < 65504), and slices take the short way
+    static constexpr int FAST = 127 + 7;
     __device__ __forceinline__ static uint32_t of(int b) {
         return kHalf ? (uint32_t)(b - 112) * 0x04000400u : (uint32_t)(b + 120) * 0x00800080u;
     }
@@ -97,6 +99,55 @@ struct PairScale {
         return twice16((uint32_t)b << 7);                             // 2^e as bf16
     }
 };
+
+// Elements of V that are no finite numbers of q's type (NaN, and beyond fp16's
+// range infinities) cannot stay in a tile of which some query sees only a part:
+// a hidden key's weight is 0, and 0 * NaN is NaN.  The converting warps take
+// them out and note where they begin: for each dim the first position of an
+// element that is +inf or NaN, and of one that is -inf or NaN.  The output takes
+// them from there (both: NaN).  An entry is the item's tag in its high and ~position
+// in its low half, so the largest of a slot is its newest item's first position,
+// and no slot is ever cleared.
+struct Aside {
+    unsigned long long* at = nullptr;   // [2][D] entries of the item's slot; null: elements stay in the tile
+    uint32_t* any = nullptr;            // the tag, once there is an entry
+    uint32_t tag = 0;
+    int t0 = 0;                         // position of the slice's first row
+    bool scan = false;                  // per-tensor caches: the slice has keys that some query of the item does not see
+};
+
+__device__ __forceinline__ unsigned long long aside_entry(uint32_t tag, int position) {
+    return (unsigned long long)tag << 32 | (0xffffffffu - (uint32_t)position);
+}
+// Whether a query at pos sees the entry's element.
+__device__ __forceinline__ bool aside_seen(unsigned long long entry, uint32_t tag, int pos) {
+    return (uint32_t)(entry >> 32) == tag && (int)(0xffffffffu - (uint32_t)entry) <= pos;
+}
+
+// 16 converted elements of the row at position t, dims d .. d + 15: those that are
+// not finite become zeros and entries.  (In place: a role of a kernel that shares
+// its registers out calls no functions.)
+template <typename T, int D>
+__device__ __forceinline__ void take_out(uint32_t (&w)[8], const Aside& aside, int t, int d) {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    const unsigned long long entry = aside_entry(aside.tag, t);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const uint32_t x = w[k / 2] >> (16 * (k & 1));
+        if ((x & kExp) == kExp) {
+            const bool nan = (x & 0x7fffu) > kExp, negative = x & 0x8000u;
+            if (nan || !negative) atomicMax(aside.at + d + k, entry);
+            if (nan || negative) atomicMax(aside.at + D + d + k, entry);
+            w[k / 2] &= k & 1 ? 0xffffu : 0xffff0000u;
+            *aside.any = aside.tag;
+        }
+    }
+}
+// Whether one of 16 codes is 0x7f or 0xff.
+__device__ __forceinline__ bool has_nan_code(const uint4& c) {
+    auto carry = [](uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; };     // into bit 7 of the byte
+    return ((carry(c.x) | carry(c.y) | carry(c.z) | carry(c.w)) & 0x80808080u) != 0;
+}
 
 // One warp's 32 rows of a 128-key tile: bulk copies bring them from their
 // blocks into the warp's own staging slot (each block's rows, then its scale
@@ -150,12 +201,18 @@ struct SliceConverter {
 
     // The slot at shared address `slot` into a tile, its rows from address `tile`
     // on; rows at or past n, and rows of the blocks in `missing`, become zeros.
-    __device__ __forceinline__ void run(uint32_t slot, uint32_t tile, int n, uint32_t missing, int lane) const {
+    __device__ __forceinline__ void run(uint32_t slot, uint32_t tile, int n, uint32_t missing, int lane,
+                                        const Aside& aside = Aside()) const {
         bool plain = n >= ROWS && missing == 0;
         if constexpr (kRow) {
             // lane r looks at row r's scale
             const uint32_t far = (uint32_t)(lds8(slot + (lane / BS) * TILE + BS * D + lane % BS) - P::LO);
-            plain = __all_sync(0xffffffffu, far <= (uint32_t)(P::HI - P::LO)) && plain;
+            plain = __all_sync(0xffffffffu, far <= (uint32_t)(P::FAST - P::LO)) && plain;
+        } else if (aside.scan && plain) {
+            bool nan = false;
+#pragma unroll 4
+            for (int j = 0; j < NJ; ++j) nan |= has_nan_code(lds128(slot + src + j * D));
+            plain = !__any_sync(0xffffffffu, nan);
         }
         const uint32_t to = tile + dst;
         if (plain) {
@@ -205,6 +262,12 @@ struct SliceConverter {
                     uint32_t* o[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
 #pragma unroll
                     for (int k = 0; k < 8; ++k) *o[k] = P::kHalf ? mul_f16x2(*o[k], m2) : mul_bf16x2(*o[k], m2);
+                }
+                if (aside.at && (kRow ? b > P::FAST : has_nan_code(c))) {
+                    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    take_out<T, D>(w, aside, aside.t0 + r0 + u, (int)(src - (r0 / BS) * TILE) % D);
+                    lo = make_uint4(w[0], w[1], w[2], w[3]);
+                    hi = make_uint4(w[4], w[5], w[6], w[7]);
                 }
                 put(to ^ (uint32_t)(j * 144), lo, hi);
             }

@@ -116,7 +116,13 @@ struct PrefillShape {
     static constexpr uint32_t NBAR = 2 * IR + 4 + 2 * (KST + VST) + 10 + (kConvert ? 6 : 0);
     static constexpr uint32_t OFF_ITEMS = (OFF_BAR + 8 * NBAR + 63) / 64 * 64;   // item ring, 64 bytes a slot
     static constexpr uint32_t OFF_HOLD = OFF_ITEMS + 64 * IR;                   // tensor-memory address
-    static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;  // 1 KB alignment slack
+    // E4M3 caches: entries of V's elements that are not finite ([slot][2][D]) and a
+    // tag a slot.  Item j has slot j % ASLOTS: while a softmax warp is at item j the
+    // converting warps are at item j + 2 at most (item j + 3 takes the ring slot of
+    // item j + 1, which that warp has yet to take).
+    static constexpr int ASLOTS = IR + 1;
+    static constexpr uint32_t OFF_ASIDE = OFF_HOLD + 16, ASIDE_BYTES = kConvert ? ASLOTS * 2 * D * 8 + 16 : 0;
+    static constexpr uint32_t SMEM = OFF_ASIDE + ASIDE_BYTES + 1024;  // 1 KB alignment slack
     // E4M3 caches: warps that convert, and the registers of the softmax's two
     // warpgroups and of the two others
     static constexpr int kConvertWarps = 6, kSoftmaxRegs = 168, kSideRegs = 88;
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar_s(x), 1);
             mbar_init(bar_p(x), 128);
-            mbar_init(bar_o(x), 1);
+            mbar_init(bar_o(x), kConvert ? 2 : 1);
             mbar_init(bar_ofree(x), 128);
         }
         mbar_init(bar_vz, 1);
@@ -226,6 +232,11 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
             for (int k = 0; k < S::kConvertWarps; ++k) mbar_init(bar_stg(k), 1);
         fence_mbar_init();
     }
+    // the words after the entries: tags of the slots that have any (items count from 1)
+    unsigned long long* aside0 = reinterpret_cast<unsigned long long*>(smem + S::OFF_ASIDE);
+    uint32_t* aside_any = reinterpret_cast<uint32_t*>(aside0 + S::ASLOTS * 2 * D);
+    if constexpr (kConvert)
+        for (uint32_t i = threadIdx.x; i < S::ASIDE_BYTES / 8; i += blockDim.x) aside0[i] = 0;
     if (threadIdx.x == 32) {
         tc05::prefetch_tmap(&tm_q);
         if constexpr (!kConvert) {
@@ -413,7 +424,11 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                         for (int k = 0; k < N / 16; ++k)
                             tc05::mma_ts(base + S::TM_O, base + S::TM_S + 8 * k, vd + (uint64_t)(k * 128), idesc_pv,
                                          (i > 0 || k > 0) ? 1u : 0u);
-                        if (i == (x ? nT1 : nT0) - 1) tc05::commit(bar_o(x));
+                        if (i == (x ? nT1 : nT0) - 1) {
+                            tc05::commit(bar_o(x));
+                            // (and what the converting warps noted of the tiles waited for above)
+                            if constexpr (kConvert) tcsm::mbar_arrive(bar_o(x));
+                        }
                         return true;
                     };
                     if (!mbar_wait_bounded(bar_qfull(0), qx[0] & 1, wl)) { ok = false; break; }
@@ -475,6 +490,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
             int j = 0, jt = 0, t = 0, nT = 0, w = cw % kStreamWarps;
             int phys[BPW];
             uint32_t missing = 0;
+            Aside aside;                         // of V's warps
             bool more = true;
             auto begin_item = [&]() {
                 more = take_item(j, it);
@@ -482,6 +498,11 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                 more = it.s >= 0;
                 t = 0;
                 nT = max(it.nT0, it.nT1);
+                if (is_v) {
+                    aside.tag = (uint32_t)j + 1;
+                    aside.at = aside0 + (j % S::ASLOTS) * 2 * D;
+                    aside.any = aside_any + j % S::ASLOTS;
+                }
             };
             // block ids of the item's tiles ids_t .. + TPE - 1 (lane l: the l-th
             // block) and of the TPE tiles after them
@@ -540,7 +561,9 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                     ok = false;
                     break;
                 }
-                conv.run(slot, (is_v ? v_base(st) : k_base(st)) + w * (32 * 128), it.L - t * N - 32 * w, missing, lane);
+                aside.t0 = t * N + 32 * w;
+                aside.scan = is_v && aside.t0 + 31 > it.L - it.n + it.i0;     // past the item's first query
+                conv.run(slot, (is_v ? v_base(st) : k_base(st)) + w * (32 * 128), it.L - aside.t0, missing, lane, aside);
                 fence_proxy_async();             // before the tensor core reads the tile
                 __syncwarp();                    // (and every lane is done with the slot)
                 if (lane == 0) mbar_arrive(is_v ? bar_vfull(st) : bar_kfull(st));
@@ -685,6 +708,28 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
             // ---- O / l to the output ----
             if (ok && warp_wait(bar_o(x), ox & 1, wl)) {
                 tc05::fence_after_sync();
+                if constexpr (kConvert) {
+                    // V's elements that are not finite, where this row sees them
+                    const uint32_t tag = (uint32_t)j + 1;
+                    if (*(volatile uint32_t*)(aside_any + j % S::ASLOTS) == tag) {
+                        const unsigned long long* at = aside0 + (j % S::ASLOTS) * 2 * D;
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t ov[32];
+                            tc05::tmem_ld32(trow + S::TM_O + cc * 32, ov);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const bool up = aside_seen(at[cc * 32 + e], tag, pos);
+                                const bool down = aside_seen(at[D + cc * 32 + e], tag, pos);
+                                if (up) ov[e] = down ? 0x7fffffffu : 0x7f800000u;
+                                else if (down) ov[e] = 0xff800000u;
+                            }
+                            tc05::tmem_st32(trow + S::TM_O + cc * 32, ov);
+                        }
+                        tc05::tmem_wait_st();
+                    }
+                }
                 const float inv = l > 0.f ? (kConvert ? p.out_scale : 1.f) / l : 0.f;
                 T* orow = reinterpret_cast<T*>(p.out) +
                           ((size_t)(it.q0 + qi) * p.num_heads + (size_t)it.g * G + (r % G)) * D;
