@@ -560,8 +560,8 @@ pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache
  * cache: every argument, check and error as there, the caches as described
  * with those formats.  Each cache element is taken in q's type: exact in bf16
  * and within fp16's range; with f16 q an element of a row cache beyond +-65504
- * becomes infinity (an f16 element from 63488 on is such a one: it was stored as
- * 65536) and one below 2^-21 may be rounded, to a multiple of 2^-24.  Here NaN
+ * (an f16 element from 63488 on is such a one: it was stored as 65536) counts as
+ * +-65504 in K and as an infinity in V, and one below 2^-21 may be rounded, to a multiple of 2^-24.  Here NaN
  * and infinite elements reach the queries that see their token and no others:
  * an infinity of V makes its dim of the output infinite, both signs NaN. */
 pkv_status paged_attention_prefill_fp8kv(void* out, const void* q, const void* k_cache, const void* v_cache,

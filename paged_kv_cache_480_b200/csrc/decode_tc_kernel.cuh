@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                     ok = false;
                     break;
                 }
-                conv.run(slot(jt), (v ? v_base(st) : k_base(st)) + wi * (32 * 128), info[0] & 0xff, (uint32_t)info[0] >> 8, lane);
+                conv.run(slot(jt), (v ? v_base(st) : k_base(st)) + wi * (32 * 128), info[0] & 0xff, (uint32_t)info[0] >> 8, lane,
+                         v == 0);
                 fence_proxy_async();             // before the tensor core reads the tile
                 __syncwarp();                    // (and every lane is done with the slot)
                 if (lane == 0) mbar_arrive(v ? bar_vfull(st) : bar_kfull(st));

@@ -37,6 +37,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
     return *reinterpret_cast<uint32_t*>(&r);
 }
+// Finite and infinite halves to +-65504 at most; NaN stays.
+__device__ __forceinline__ uint32_t clamp_f16x2(uint32_t a) {
+    const uint32_t most = 0x7bff7bffu, least = 0xfbfffbffu;
+    __half2 r = __hmin2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&most));
+    r = __hmax2_nan(r, *reinterpret_cast<const __half2*>(&least));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t twice16(uint32_t h) { return h | (h << 16); }
 
 // 16 codes as 16-bit values, lo the codes 0-7; of a row cache times the pair
@@ -200,8 +207,10 @@ struct SliceConverter {
     }
 
     // The slot at shared address `slot` into a tile, its rows from address `tile`
-    // on; rows at or past n, and rows of the blocks in `missing`, become zeros.
-    __device__ __forceinline__ void run(uint32_t slot, uint32_t tile, int n, uint32_t missing, int lane,
+    // on; rows at or past n, and rows of the blocks in `missing`, become zeros.  In
+    // fp16 elements of K beyond its range are +-65504: an infinity would leave nothing
+    // of a logit.
+    __device__ __forceinline__ void run(uint32_t slot, uint32_t tile, int n, uint32_t missing, int lane, bool is_k,
                                         const Aside& aside = Aside()) const {
         bool plain = n >= ROWS && missing == 0;
         if constexpr (kRow) {
@@ -262,6 +271,10 @@ struct SliceConverter {
                     uint32_t* o[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
 #pragma unroll
                     for (int k = 0; k < 8; ++k) *o[k] = P::kHalf ? mul_f16x2(*o[k], m2) : mul_bf16x2(*o[k], m2);
+                    if (P::kHalf && is_k && b > P::FAST) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) *o[k] = clamp_f16x2(*o[k]);
+                    }
                 }
                 if (aside.at && (kRow ? b > P::FAST : has_nan_code(c))) {
                     uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};

@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                 }
                 aside.t0 = t * N + 32 * w;
                 aside.scan = is_v && aside.t0 + 31 > it.L - it.n + it.i0;     // past the item's first query
-                conv.run(slot, (is_v ? v_base(st) : k_base(st)) + w * (32 * 128), it.L - aside.t0, missing, lane, aside);
+                conv.run(slot, (is_v ? v_base(st) : k_base(st)) + w * (32 * 128), it.L - aside.t0, missing, lane, !is_v,
+                         aside);
                 fence_proxy_async();             // before the tensor core reads the tile
                 __syncwarp();                    // (and every lane is done with the slot)
                 if (lane == 0) mbar_arrive(is_v ? bar_vfull(st) : bar_kfull(st));

@@ -128,3 +128,33 @@ def test_v_rows_from_the_end_of_fp16(D, bs, G):
     out = check("paged_attention_prefill_fp8row", lens, counts, Hkv * G, D, bs, "f16", kc, vc, bt,
                 lambda c, s, L: rm.sequence(c, bs, D, bt, s, L), q, D ** -0.5)
     assert out[:70].isfinite().all() and (out[70:200, :G, 3] == math.inf).all() and out[200:300, :G, 3].isnan().all()
+
+
+def large_keys(x, g):
+    x = x * 1000.0
+    x[::7, :, 0] = 65504.0                       # stored as 65536
+    x[3::7, :, 1] = -63488.0
+    x[5::50, :, 2] = 90000.0                     # as a rotated f16 key may be
+    return x
+
+
+@pytest.mark.parametrize("D,bs,G", [(64, 16, 1), (128, 32, 8)])
+def test_k_elements_from_the_end_of_fp16_in_chunks(D, bs, G):
+    lens, counts, Hkv = [300, 77], [140, 77], 2
+    kc, vc, bt, cl, gc = paged_rows(lens, Hkv * G, Hkv, D, bs, "f16", 74, kscale=large_keys)
+    q = torch.randn(sum(counts), Hkv * G, D, generator=gc, device="cuda").half()
+    check("paged_attention_prefill_fp8row", lens, counts, Hkv * G, D, bs, "f16", kc, vc, bt,
+          lambda c, s, L: rm.sequence(c, bs, D, bt, s, L), q, 1e-5)
+
+
+@pytest.mark.parametrize("D,bs,G", [(64, 16, 20), (128, 32, 64)])
+def test_k_elements_from_the_end_of_fp16_in_decode(D, bs, G):
+    lens = [300, 77, 1000]
+    kc, vc, bt, cl, gc = paged_rows(lens, 2 * G, 2, D, bs, "f16", 75, kscale=large_keys)
+    q = torch.randn(3, 2 * G, D, generator=gc, device="cuda").half()
+    out = torch.empty_like(q)
+    pkv.paged_attention_decode_fp8row(out, q, kc, vc, bt, cl, 1e-5)
+    for s, L in enumerate(lens):
+        K, V = (rm.sequence(c, bs, D, bt, s, L) for c in (kc, vc))
+        ref, logit, top = masked_reference(q[s:s + 1], K, V, 1e-5, torch.float16)
+        rm.close(out[s:s + 1], ref, rm.attention_bound(ref, logit, top, torch.float16, torch.float16, L) + 2.0 ** -25)
