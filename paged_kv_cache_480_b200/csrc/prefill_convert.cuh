@@ -131,24 +131,34 @@ __device__ __forceinline__ bool aside_seen(unsigned long long entry, uint32_t ta
     return (uint32_t)(entry >> 32) == tag && (int)(0xffffffffu - (uint32_t)entry) <= pos;
 }
 
-// 16 converted elements of the row at position t, dims d .. d + 15: those that are
-// not finite become zeros and entries.  (In place: a role of a kernel that shares
-// its registers out calls no functions.)
+// 16 codes of the row with scale byte b (per-tensor caches: 127) at position t, dims d
+// .. d + 15: those that are not finite in T become zeros and entries.  A loop, and
+// nothing unrolled: it hardly ever runs, and the code around it has to stay in the
+// instruction caches.  (In place: a role of a kernel that shares its registers out
+// calls no functions.)
 template <typename T, int D>
-__device__ __forceinline__ void take_out(uint32_t (&w)[8], const Aside& aside, int t, int d) {
-    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+__device__ __forceinline__ void take_out(uint4& c, int& b, const Aside& aside, int t, int d) {
     const unsigned long long entry = aside_entry(aside.tag, t);
-#pragma unroll
+    const float most = (std::is_same<T, __half>::value ? 65504.f : INFINITY), scale = row_scale(b);
+#pragma unroll 1
     for (int k = 0; k < 16; ++k) {
-        const uint32_t x = w[k / 2] >> (16 * (k & 1));
-        if ((x & kExp) == kExp) {
-            const bool nan = (x & 0x7fffu) > kExp, negative = x & 0x8000u;
-            if (nan || !negative) atomicMax(aside.at + d + k, entry);
-            if (nan || negative) atomicMax(aside.at + D + d + k, entry);
-            w[k / 2] &= k & 1 ? 0xffffu : 0xffff0000u;
+        const uint32_t code = c.x & 0xffu;
+        const uint32_t h = e4m3x2_to_f16x2((uint16_t)code);
+        const float x = __half2float(__ushort_as_half((unsigned short)(h & 0xffffu))) * scale;
+        const bool fine = fabsf(x) <= most;
+        if (!fine) {
+            if (!(x < 0.f)) atomicMax(aside.at + d + k, entry);
+            if (!(x > 0.f)) atomicMax(aside.at + D + d + k, entry);
             *aside.any = aside.tag;
         }
+        // the next code to the front, this one (or zero) to the end
+        const uint32_t last = fine ? code : 0u;
+        c.x = __funnelshift_r(c.x, c.y, 8);
+        c.y = __funnelshift_r(c.y, c.z, 8);
+        c.z = __funnelshift_r(c.z, c.w, 8);
+        c.w = __funnelshift_r(c.w, last, 8);
     }
+    if (b == kRowScaleNan) b = 127;
 }
 // Whether one of 16 codes is 0x7f or 0xff.
 __device__ __forceinline__ bool has_nan_code(const uint4& c) {
@@ -263,6 +273,8 @@ struct SliceConverter {
                     c = make_uint4(0u, 0u, 0u, 0u);
                     b = 127;
                 }
+                if (aside.at && (kRow ? b > P::FAST : has_nan_code(c)))
+                    take_out<T, D>(c, b, aside, aside.t0 + r0 + u, (int)(src - (r0 / BS) * TILE) % D);
                 const bool in = b >= P::LO && b <= P::HI;
                 uint4 lo, hi;
                 convert16<T, kRow>(c, in ? P::of(b) : P::first(b), factors, lo, hi);
@@ -275,12 +287,6 @@ struct SliceConverter {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) *o[k] = clamp_f16x2(*o[k]);
                     }
-                }
-                if (aside.at && (kRow ? b > P::FAST : has_nan_code(c))) {
-                    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    take_out<T, D>(w, aside, aside.t0 + r0 + u, (int)(src - (r0 / BS) * TILE) % D);
-                    lo = make_uint4(w[0], w[1], w[2], w[3]);
-                    hi = make_uint4(w[4], w[5], w[6], w[7]);
                 }
                 put(to ^ (uint32_t)(j * 144), lo, hi);
             }

@@ -715,18 +715,16 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                     if (*(volatile uint32_t*)(aside_any + j % S::ASLOTS) == tag) {
                         const unsigned long long* at = aside0 + (j % S::ASLOTS) * 2 * D;
 #pragma unroll 1
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            uint32_t ov[32];
-                            tc05::tmem_ld32(trow + S::TM_O + cc * 32, ov);
+                        for (int d = 0; d < D; d += 8) {
+                            uint32_t ov[8];
+                            tc05::tmem_ld8(trow + S::TM_O + d, ov);
                             tc05::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const bool up = aside_seen(at[cc * 32 + e], tag, pos);
-                                const bool down = aside_seen(at[D + cc * 32 + e], tag, pos);
-                                if (up) ov[e] = down ? 0x7fffffffu : 0x7f800000u;
-                                else if (down) ov[e] = 0xff800000u;
+                            for (int e = 0; e < 8; ++e) {
+                                const bool up = aside_seen(at[d + e], tag, pos), down = aside_seen(at[D + d + e], tag, pos);
+                                if (up || down) ov[e] = up && down ? 0x7fffffffu : up ? 0x7f800000u : 0xff800000u;
                             }
-                            tc05::tmem_st32(trow + S::TM_O + cc * 32, ov);
+                            tc05::tmem_st8(trow + S::TM_O + d, ov);
                         }
                         tc05::tmem_wait_st();
                     }
