@@ -185,8 +185,9 @@ pkv_status paged_attention_decode_append(void* out, const void* q, const void* k
  * q and out in `dtype` (f32, f16 or bf16).  Workspace, partitioning, checks
  * and errors as for paged_attention_decode (the workspace size does not
  * depend on the cache type).  With 16-bit q the products run on the tensor
- * cores in fp16 (E4M3 is exact in fp16; bf16 q is rounded to fp16 there, so
- * |q| must stay below 65504).
+ * cores in fp16 (E4M3 is exact in fp16; bf16 q goes in times a power of two where
+ * fp16's range asks for it, one for up to 8 heads of a group: elements below 2^-15
+ * of their largest are off by at most 2^-23 of it).
  *
  * reshape_and_cache_fp8kv: reshape_and_cache into such caches: each element
  * x of key (value) becomes e4m3(x / k_scale) (resp. v_scale), the quotient
@@ -232,8 +233,8 @@ pkv_status reshape_and_cache_fp8kv(const void* key, const void* value, void* k_c
  * paged_attention_decode_fp8row: paged_attention_decode over such caches.  The
  * softmax weights are taken relative to the largest weight times V scale, so
  * rows of very different scales keep their precision.  With 16-bit q the
- * products run on the tensor cores in fp16 (bf16 q is rounded to fp16 there,
- * so |q| must stay below 65504).  With 16-bit q, G >= 17, scale > 0 and partition_size 0
+ * products run on the tensor cores in fp16; bf16 q goes in times a power
+ * of two as over the per-tensor cache.  With 16-bit q, G >= 17, scale > 0 and partition_size 0
  * the call takes the tcgen05 kernel, in q's type: weights are rounded to it,
  * and elements are taken in it as in paged_attention_prefill_fp8row.
  * Workspace, partitioning, checks and errors as for paged_attention_decode.

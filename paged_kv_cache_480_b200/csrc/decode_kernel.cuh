@@ -538,8 +538,13 @@ struct MmaConsumer {
 
 // ===========================================================================
 // Tensor-core consumer for an FP8 (E4M3) cache and 16-bit q/out, G in {4, 8}.
-// E4M3 converts exactly to fp16, so both products run as fp16 mma.m16n8k16
-// (q is rounded to fp16 when it is bf16).  Fragment layout as in
+// E4M3 converts exactly to fp16, so both products run as fp16 mma.m16n8k16.  bf16
+// q whose largest element (of the item's heads) is not in [2^-2, 2^15) goes in
+// times a power of two that brings that to [2^8, 2^9), and the logits take the
+// inverse: elements of 2^-15 of it and more keep all their bits, smaller ones
+// are off by at most 2^-23 of it.  (A power for each head costs a second register
+// and a multiply a slice: 40 MHA heads over row caches 142.9 us, so 141.0, bf16
+// rounded to fp16 as it is 140.5.)  Fragment layout as in
 // MmaConsumer, with 16 dims per 16-byte chunk of a cache row:
 //   QK step (j, hf): k-slots (2c, 2c+1) <-> dims 16(4j+c) + 4hf + {0,1},
 //                    k-slots (2c+8, 2c+9) <-> dims 16(4j+c) + 4hf + {2,3};
@@ -573,6 +578,8 @@ struct MmaConsumerFp8 {
     uint32_t qf[KJ][8];                    // fp16 pairs: [hf][b0, b1] for hf = 0..3
     float o[MT][4];
     float m0, m1, l0, l1;
+    static constexpr bool kScaleQ = !std::is_same<TQ, __half>::value;
+    float sq;                              // bf16 q: scale_log2 over the item's power of two
 
     __device__ __forceinline__ static void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -587,13 +594,13 @@ struct MmaConsumerFp8 {
         asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
         return d;
     }
-    __device__ __forceinline__ static uint32_t to_f16x2(uint32_t w) {
-        if constexpr (std::is_same<TQ, __half>::value) {
+    __device__ __forceinline__ static uint32_t to_f16x2(uint32_t w, float mult) {
+        if constexpr (!kScaleQ) {
             return w;
         } else {
             float lo, hi;
             Elem<__nv_bfloat16>::widen2(w, lo, hi);
-            return Elem<__half>::pack2(lo, hi);
+            return Elem<__half>::pack2(lo * mult, hi * mult);
         }
     }
     __device__ __forceinline__ static float lo_f(uint32_t w) {
@@ -608,6 +615,7 @@ struct MmaConsumerFp8 {
         c = lane & 3;
         m0 = m1 = kNoMax;
         l0 = l1 = 0.f;
+        if constexpr (kScaleQ) sq = 0.f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
 #pragma unroll
@@ -616,7 +624,8 @@ struct MmaConsumerFp8 {
             for (int i = 0; i < 8; ++i) qf[j][i] = 0u;
     }
 
-    __device__ __forceinline__ void begin(const unsigned char* qslot, float, int nh) {
+    __device__ __forceinline__ void begin(const unsigned char* qslot, float scale_log2, int nh) {
+        uint32_t top = 0;                           // largest |q| of the lane, as bf16 bits
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
             uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
@@ -627,7 +636,30 @@ struct MmaConsumerFp8 {
             }
             const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) qf[j][i] = to_f16x2(w[i]);
+            for (int i = 0; i < 8; ++i) {
+                qf[j][i] = w[i];
+                if constexpr (kScaleQ) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+            }
+        }
+        if constexpr (kScaleQ) {
+            uint32_t x = max(top & 0xffffu, top >> 16);
+            if (x >= 0x7f80u) x = 0u;               // NaN and infinity stay what they are under any factor
+            x = __reduce_max_sync(kFull, x) >> 7;   // its exponent byte
+            sq = scale_log2;
+            if (x - 125u > 141u - 125u) {
+                const uint32_t up = min(254u + 8u - x, 253u);       // (the factor and its inverse are normal numbers)
+                const float mult = __uint_as_float(up << 23);
+                sq *= __uint_as_float((254u - up) << 23);
+#pragma unroll
+                for (int j = 0; j < KJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) qf[j][i] = to_f16x2(qf[j][i], mult);
+            } else {
+#pragma unroll
+                for (int j = 0; j < KJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) qf[j][i] = to_f16x2(qf[j][i], 1.f);
+            }
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -673,18 +705,19 @@ struct MmaConsumerFp8 {
                                            float (&z)[4]) const {
         const bool v0 = r < nvalid, v8 = r + 8 < nvalid;
         if constexpr (kRow) {
-            const float a = scale_log2 * row_scale(rs.k0), b = scale_log2 * row_scale(rs.k8);
             const float ya = row_exponent(rs.v0), yb = row_exponent(rs.v8);
+            const float s = kScaleQ ? sq : scale_log2, a = s * row_scale(rs.k0), b = s * row_scale(rs.k8);
             z[0] = v0 ? fmaf(sc[0], a, ya) : -INFINITY;
             z[1] = v0 ? fmaf(sc[1], a, ya) : -INFINITY;
             z[2] = v8 ? fmaf(sc[2], b, yb) : -INFINITY;
             z[3] = v8 ? fmaf(sc[3], b, yb) : -INFINITY;
             return;
         }
-        z[0] = v0 ? sc[0] * scale_log2 : -INFINITY;
-        z[1] = v0 ? sc[1] * scale_log2 : -INFINITY;
-        z[2] = v8 ? sc[2] * scale_log2 : -INFINITY;
-        z[3] = v8 ? sc[3] * scale_log2 : -INFINITY;
+        const float s = kScaleQ ? sq : scale_log2;
+        z[0] = v0 ? sc[0] * s : -INFINITY;
+        z[1] = v0 ? sc[1] * s : -INFINITY;
+        z[2] = v8 ? sc[2] * s : -INFINITY;
+        z[3] = v8 ? sc[3] * s : -INFINITY;
     }
 
     // Weights of a slice against the new maxima (fp16 pairs), added to l, and
