@@ -172,20 +172,24 @@ def _contig(t, name):
 # workspace: one zero-initialised buffer per device, grown on demand
 # ---------------------------------------------------------------------------
 _workspaces = {}
-_outgrown = []          # (graphs that were captured with them may still be replayed)
+_outgrown = []          # (graphs that were captured with them may still be replayed; each is at most half the next)
+_COUNTER_BYTES = 256    # a workspace's first bytes, the only ones that must be zero (pagedkv.h)
 
 
-def default_workspace(device, nbytes):
+def default_workspace(device, nbytes, stream=None):
     """The binding's per-device workspace (not for concurrent streams).  It is
-    ready on every stream; a call that needs a larger one while its stream is
-    captured gets a workspace of the graph's own, zeroed at each replay."""
+    ready on every stream; a call that needs a larger one while its stream
+    (``stream``, or the current one) is captured gets a workspace of the graph's
+    own, whose counters each replay zeroes."""
     import torch
     idx = device.index if device.index is not None else torch.cuda.current_device()
     ws = _workspaces.get(idx)
     if ws is None or ws.numel() < nbytes:
-        with torch.cuda.device(idx):
+        with torch.cuda.device(idx), torch.cuda.stream(stream):
             if torch.cuda.is_current_stream_capturing():
-                return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                ws[:_COUNTER_BYTES].zero_()
+                return ws
             size = max(nbytes, 1 << 20, 0 if ws is None else 2 * ws.numel())
             if ws is not None:
                 _outgrown.append(ws)
@@ -239,7 +243,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     if need == 0:
         raise PagedKVError(2, "paged_attention_workspace_size")
     if workspace is None:
-        workspace = default_workspace(q.device, need)
+        workspace = default_workspace(q.device, need, stream)
     st = lib.paged_attention_decode(
         _contig(out, "out"), _contig(q, "q"), _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"),
         _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"),
@@ -282,7 +286,7 @@ def paged_attention_decode_append(out, q, key, value, k_cache, v_cache, slot_map
     if need == 0:
         raise PagedKVError(2, "paged_attention_workspace_size")
     if workspace is None:
-        workspace = default_workspace(q.device, need)
+        workspace = default_workspace(q.device, need, stream)
     st = lib.paged_attention_decode_append(
         _contig(out, "out"), _contig(q, "q"), _cuda(key, "key"), _cuda(value, "value"),
         _contig(k_cache, "k_cache"), _contig(v_cache, "v_cache"), _contig(slot_mapping, "slot_mapping"),
@@ -322,7 +326,7 @@ def paged_attention_decode_fp8kv(out, q, k_cache, v_cache, block_tables, context
     if need == 0:
         raise PagedKVError(2, "paged_attention_workspace_size")
     if workspace is None:
-        workspace = default_workspace(q.device, need)
+        workspace = default_workspace(q.device, need, stream)
     st = lib.paged_attention_decode_fp8kv(
         _contig(out, "out"), _contig(q, "q"), _fp8_cache(k_cache, "k_cache"), _fp8_cache(v_cache, "v_cache"),
         _contig(block_tables, "block_tables"), _contig(context_lens, "context_lens"), float(scale),
@@ -542,7 +546,7 @@ def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, contex
         need = _fast.paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
         if need == 0:
             raise PagedKVError(2, "paged_attention_workspace_size")
-        workspace = default_workspace(q.device, need)
+        workspace = default_workspace(q.device, need, stream)
     _call("paged_attention_decode_fp8row", dev, stream, _on(dev, out, "out"), _on(dev, q, "q"),
           _on(dev, k_cache, "k_cache"), _on(dev, v_cache, "v_cache"), _on(dev, block_tables, "block_tables"),
           _on(dev, context_lens, "context_lens"), scale, Hkv, bs, S, H, D, NB, MB, max_context_len, code,
