@@ -37,15 +37,18 @@ _fast = None            # the _fastcall extension, bound to _lib
 _lock = threading.Lock()
 
 
+def _built(path):
+    if not os.path.exists(path):
+        raise FileNotFoundError(f"{path} is missing: build it with `python -m paged_kv_cache_480_b200.build`")
+
+
 def load_library(path=LIB_PATH):
     """Open libpagedkv.so (once).  Raises if it has not been built."""
     global _lib, _fast
     with _lock:
         if _lib is not None:
             return _lib
-        for p in (path, FASTCALL_PATH):
-            if not os.path.exists(p):
-                raise FileNotFoundError(f"{p} is missing: build it with `python -m paged_kv_cache_480_b200.build`")
+        _built(path)
         lib = ctypes.CDLL(path)
         P, I, I64, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         lib.pkv_status_string.argtypes = [I]
@@ -128,12 +131,30 @@ def load_library(path=LIB_PATH):
         lib.pkv_bm_ref_count.restype = I
         lib.pkv_bm_utilisation.argtypes = [P]
         lib.pkv_bm_utilisation.restype = ctypes.c_double
-        from . import _fastcall
-        for name in dir(_fastcall):
-            if name != "bind" and not name.startswith("_"):
-                _fastcall.bind(name, ctypes.cast(getattr(lib, name), P).value)
-        _lib, _fast = lib, _fastcall
+        if os.path.exists(FASTCALL_PATH):
+            _fast = _bind_fast(lib)
+        _lib = lib
         return lib
+
+
+def _bind_fast(lib):
+    from . import _fastcall
+    for name in dir(_fastcall):
+        if name != "bind" and not name.startswith("_"):
+            _fastcall.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+    return _fastcall
+
+
+def _load_fast():
+    """The extension of the calls that pass plain numbers.  Raises if it has not
+    been built; the other calls do without it."""
+    global _fast
+    lib = load_library()
+    with _lock:
+        if _fast is None:
+            _built(FASTCALL_PATH)
+            _fast = _bind_fast(lib)
+    return _fast
 
 
 def _check(status, what):
@@ -463,7 +484,7 @@ def _call(name, dev, stream, *args):
     """One library call on GPU dev, its stream last; raises on a bad status."""
     torch = _torch()
     if _fast is None:
-        load_library()
+        _load_fast()
     if torch._C._cuda_getDevice() != dev:       # launches go to the current device
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
@@ -542,7 +563,7 @@ def paged_attention_decode_fp8row(out, q, k_cache, v_cache, block_tables, contex
     code = _code(dtype)
     if workspace is None:
         if _fast is None:
-            load_library()
+            _load_fast()
         need = _fast.paged_attention_workspace_size(S, H, Hkv, D, bs, max_context_len, code, partition_size)
         if need == 0:
             raise PagedKVError(2, "paged_attention_workspace_size")

@@ -7,7 +7,8 @@ parallel and links them, with the host block manager, into
 Objects go to ``paged_kv_cache_480_b200/_build/``; a unit is rebuilt when it
 or any header is newer than its object.  ``_fastcall.*.so`` beside it is a small
 CPython extension through which the binding makes the calls that are issued
-once a layer and step.
+once a layer and step; where Python's headers are missing it is left out, and
+those calls say so.
 """
 import glob
 import importlib.machinery
@@ -81,10 +82,12 @@ def build(force=False, verbose=False, extra_nvcc=()):
         tmp = LIB + f".tmp{os.getpid()}"
         _run([_nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
-    src = os.path.join(CSRC, "py", "fastcall.cpp")
-    if force or _stale(src, FASTCALL, glob.glob(os.path.join(INCLUDE, "*.h"))):
+    src, python = os.path.join(CSRC, "py", "fastcall.cpp"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        print(f"no Python.h in {python}: {os.path.basename(FASTCALL)} is not built", file=sys.stderr)
+    elif force or _stale(src, FASTCALL, glob.glob(os.path.join(INCLUDE, "*.h"))):
         tmp = FASTCALL + f".tmp{os.getpid()}"
-        _run(["g++"] + CXX_FLAGS + ["-I", sysconfig.get_paths()["include"], "-shared", "-o", tmp, src])
+        _run(["g++"] + CXX_FLAGS + ["-I", python, "-shared", "-o", tmp, src])
         os.replace(tmp, FASTCALL)
     return LIB
 
