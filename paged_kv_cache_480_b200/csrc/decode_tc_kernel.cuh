@@ -488,17 +488,13 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                 const uint64_t dv = tc05::smem_desc(v_base(0), S::KV_HALF, 1024);
                 TcSegWalk w = walk0;
                 bool ok = true;
-                int jt = 0, js = 0, vzc = 0;
+                int jt = 0, js = 0;
                 int px[2] = {0, 0};                          // P_x phases consumed
                 int ox[2] = {0, 0};                          // units whose O_x accumulation began
-                struct Pend { int jt, x, first, last, vz; } prev = {-1, 0, 0, 0, 0};
+                struct Pend { int jt, x, first, last; } prev = {-1, 0, 0, 0};
                 auto pv = [&](const Pend& e) -> bool {       // O_x += P_x V_jt
                     const int sv = e.jt % VST;
                     if (!mbar_wait_bounded(bar_vfull(sv), (e.jt / VST) & 1, wl)) return false;
-                    if (e.vz) {
-                        if (!mbar_wait_bounded(bar_vz, vzc & 1, wl)) return false;
-                        ++vzc;
-                    }
                     if (!mbar_wait_bounded(bar_p(e.x), px[e.x] & 1, wl)) return false;
                     ++px[e.x];
                     if (e.first) {
@@ -522,8 +518,6 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                 while (ok && w.next(p, s, u, t0, n, L, Ts)) {
                     const int b = js & 1;
                     if (!mbar_wait_bounded(bar_qfull(b), (js >> 1) & 1, wl)) { ok = false; break; }
-                    const int nblk = (L + BS - 1) / BS;
-                    const bool unit_vz = !kConvert && t0 + n == Ts && L - (Ts - 1) * N < min(nblk * BS - (Ts - 1) * N, N);
                     for (int i = 0; i < n; ++i, ++jt) {
                         const int x = jt & 1;
                         if (!mbar_wait_bounded(bar_kfull(jt % KST), (jt / KST) & 1, wl)) { ok = false; break; }
@@ -545,7 +539,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                         if (i == n - 1) tc05::commit(bar_qempty(b));
                         if (prev.jt >= 0 && !pv(prev)) { ok = false; break; }
                         // this tile's half: its first tile of the unit are i = 0, 1, its last i = n-2, n-1
-                        prev = {jt, x, i < 2 ? 1 : 0, i >= n - 2 ? 1 : 0, (unit_vz && i == n - 1) ? 1 : 0};
+                        prev = {jt, x, i < 2 ? 1 : 0, i >= n - 2 ? 1 : 0};
                     }
                     ++js;
                 }
@@ -563,24 +557,28 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
             TcSegWalk w = walk0;
             int jt = 0, js = 0, qloads[2] = {0, 0};
             bool ok = true;
-            // V rows of the pending tile past its context end, zeroed once it lands
-            int vz_jt = -1, vz_r0 = 0, vz_r1 = 0;
+            // V rows past a context's end in its last block hold whatever the pool holds
+            // there.  The tile with them lands on a barrier of this warp's own, which
+            // then zeroes them and completes the stage.  (Announced to the MMA thread
+            // on a barrier of its own the zeroings of short units could run two phases
+            // ahead of its waits, which go by parity, and never end.)
+            int vz_jt = -1, vz_r0 = 0, vz_r1 = 0, vz_n = 0;     // the pending tile and its rows; tiles zeroed
             auto do_vz = [&]() {
-                const int st = vz_jt % VST;
-                if (warp_wait(bar_vfull(st), (vz_jt / VST) & 1, wl)) {
-                    const int rows = vz_r1 - vz_r0;
-                    for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
-                        const int dh = i / (rows * 8);
-                        const int rem = i - dh * rows * 8;
-                        *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
-                                                  (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_vz);
-                } else {
+                if (!warp_wait(bar_vz, vz_n & 1, wl)) {
                     ok = false;
+                    return;
                 }
+                const int st = vz_jt % VST, rows = vz_r1 - vz_r0;
+                for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
+                    const int dh = i / (rows * 8);
+                    const int rem = i - dh * rows * 8;
+                    *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
+                                              (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_vfull(st));
+                ++vz_n;
                 vz_jt = -1;
             };
             int s, u, t0, n, L, Ts;
@@ -621,13 +619,18 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                     const int cur_row = next_row;
                     if (i + 1 < n) next_row = tile_row(i + 1);
                     const int st = jt % nst;
-                    // the pending zeroing must happen before its stage is waited for again
-                    if (is_v && vz_jt >= 0 && jt >= vz_jt + VST) do_vz();
+                    // the unit's last tile: V rows from the context end to the end of its last block
+                    const int r0 = L - (Ts - 1) * N, r1 = min(nblk * BS - (Ts - 1) * N, N);
+                    const bool vz = is_v && t0 + i == Ts - 1 && r0 < r1;
+                    // a pending zeroing happens before its stage is waited for again, and
+                    // before the next one
+                    if (vz_jt >= 0 && (jt >= vz_jt + VST || vz)) do_vz();
+                    if (!ok) break;
                     if (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full = is_v ? bar_vfull(st) : bar_kfull(st);
+                    const uint32_t full = vz ? bar_vz : is_v ? bar_vfull(st) : bar_kfull(st);
                     const uint32_t dst = is_v ? v_base(st) : k_base(st);
                     if (lane == 0) mbar_arrive_expect_tx(full, S::KV_BYTES);
     #pragma unroll
@@ -637,27 +640,25 @@ __global__ void __launch_bounds__(kDecodeTcThreads<T, TC>, 1)
                             for (int dh = 0; dh < S::DH; ++dh)
                                 tc05::tma_load_2d(dst + dh * S::KV_HALF + bi * BS * 128, map, dh * 64, row, full);
                     }
-                    if (is_v && t0 + i == Ts - 1) {
-                        // the unit's last tile: V rows from the context end to the end of
-                        // its last block hold whatever the pool holds there
-                        const int r0 = L - (Ts - 1) * N;
-                        const int r1 = min(nblk * BS - (Ts - 1) * N, N);
-                        if (r0 < r1) {
-                            if (vz_jt >= 0) do_vz();
-                            vz_jt = jt;
-                            vz_r0 = r0;
-                            vz_r1 = r1;
-                        }
+                    if (vz) {
+                        vz_jt = jt;
+                        vz_r0 = r0;
+                        vz_r1 = r1;
                     }
                 }
                 ++js;
             }
-            if (is_v && vz_jt >= 0 && ok) do_vz();
+            if (vz_jt >= 0 && ok) do_vz();
             if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
             if (lane == 0) {
                 // every copy requested above lands before this warp leaves (the last
                 // copy into each stage and each q buffer; earlier ones were consumed
-                // before their buffer was refilled)
+                // before their buffer was refilled); a tile that is still pending
+                // completes its stage as it is
+                if (vz_jt >= 0) {
+                    mbar_wait_bounded(bar_vz, vz_n & 1, kWaitLimit);
+                    mbar_arrive(bar_vfull(vz_jt % VST));
+                }
                 for (int b = 0; b < 2; ++b)
                     if (qloads[b] > 0) mbar_wait_bounded(bar_qfull(b), (qloads[b] - 1) & 1, kWaitLimit);
                 for (int t = max(0, jt - nst); t < jt; ++t)

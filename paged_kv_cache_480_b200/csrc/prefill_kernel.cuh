@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                 const uint64_t dk = tc05::smem_desc(k_base(0), 16, 1024);
                 const uint64_t dv = tc05::smem_desc(v_base(0), S::KV_HALF, 1024);
                 bool ok = true;
-                int jt0 = 0, vzc = 0;                          // key tiles of earlier items; zeroings seen
+                int jt0 = 0;                                   // key tiles of earlier items
                 int qx[2] = {0, 0}, px[2] = {0, 0}, ox[2] = {0, 0};   // q loads, P phases, items per tile
                 for (int j = 0; ok; ++j) {
                     if (!mbar_wait_bounded(bar_ifull(j % IR), (j / IR) & 1, wl)) { ok = false; break; }
@@ -386,8 +386,6 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                     if (it.s < 0) break;
                     const int nT0 = it.nT0, nT1 = it.nT1, nT = max(nT0, nT1);
                     const bool two = nT1 > 0;
-                    const bool vz = !kConvert && it.vz_r0 < it.vz_r1;   // (converted tiles come with zeros there)
-                    const int vz_x = nT0 == nT ? 0 : 1;            // the first product reading the last V tile
                     auto qk = [&](int x, int i) {                  // S_x = Q_x K_i^T
                         const uint32_t d = tm + x * S::TM_TILE + S::TM_S;
                         const uint64_t ad = dq + (uint64_t)((x * S::Q_BYTES) >> 4);
@@ -405,10 +403,6 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                     auto pv = [&](int x, int i) -> bool {          // O_x += P_x V_i
                         const int jt = jt0 + i, sv = jt % VST;
                         if (!mbar_wait_bounded(bar_vfull(sv), (jt / VST) & 1, wl)) return false;
-                        if (vz && i == nT - 1 && x == vz_x) {
-                            if (!mbar_wait_bounded(bar_vz, vzc & 1, wl)) return false;
-                            ++vzc;
-                        }
                         if (!mbar_wait_bounded(bar_p(x), px[x] & 1, wl)) return false;
                         ++px[x];
                         if (i == 0) {
@@ -591,29 +585,35 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
             const CUtensorMap* map = is_v ? &tm_v : &tm_k;
             int jt = 0;                                  // key tiles streamed so far
             bool ok = true;
-            // V rows of the pending tile past its context end, zeroed once it lands
-            int vz_jt = -1, vz_r0 = 0, vz_r1 = 0;
+            // V rows past a context's end in its last block hold whatever the pool holds
+            // there.  The tile with them lands on a barrier of this warp's own, which
+            // then zeroes them and completes the stage.  (Announced to the MMA thread
+            // on a barrier of its own the zeroings of short items could run two phases
+            // ahead of its waits, which go by parity, and never end.)
+            int vz_jt = -1, vz_r0 = 0, vz_r1 = 0, vz_n = 0;     // the pending tile and its rows; tiles zeroed
             auto do_vz = [&]() {
-                const int st = vz_jt % VST;
-                if (warp_wait(bar_vfull(st), (vz_jt / VST) & 1, wl)) {
-                    const int rows = vz_r1 - vz_r0;
-                    for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
-                        const int dh = i / (rows * 8);
-                        const int rem = i - dh * rows * 8;
-                        *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
-                                                  (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_vz);
-                } else {
+                if (!warp_wait(bar_vz, vz_n & 1, wl)) {
                     ok = false;
+                    return;
                 }
+                const int st = vz_jt % VST, rows = vz_r1 - vz_r0;
+                for (int i = lane; i < rows * S::DH * 8; i += 32) {   // 16-byte chunks
+                    const int dh = i / (rows * 8);
+                    const int rem = i - dh * rows * 8;
+                    *reinterpret_cast<uint4*>(smem + (v_base(st) - sm) + dh * S::KV_HALF + (vz_r0 + rem / 8) * 128 +
+                                              (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_vfull(st));
+                ++vz_n;
                 vz_jt = -1;
             };
             for (int j = 0; ok; ++j) {
                 PrefillItem it;
-                if (!take_item(j, it)) { ok = false; break; }
+                // (the scheduler may be waiting, through the MMA thread, for the pending tile)
+                if (vz_jt >= 0 && !__all_sync(kAll, mbar_test_wait(bar_ifull(j % IR), (j / IR) & 1))) do_vz();
+                if (!ok || !take_item(j, it)) { ok = false; break; }
                 if (it.s < 0) break;
                 const int s = it.s, g = it.g;
                 const int nT = max(it.nT0, it.nT1);
@@ -636,13 +636,16 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                     const int cur_row = next_row;
                     if (t + 1 < nT) next_row = tile_row(t + 1);
                     const int st = jt % nst;
-                    // a pending zeroing happens before its stage is waited for again
-                    if (is_v && vz_jt >= 0 && jt >= vz_jt + VST) do_vz();
+                    const bool vz = is_v && t == nT - 1 && it.vz_r0 < it.vz_r1;   // the item's last key tile
+                    // a pending zeroing happens before its stage is waited for again, and
+                    // before the next one
+                    if (vz_jt >= 0 && (jt >= vz_jt + VST || vz)) do_vz();
+                    if (!ok) break;
                     if (jt >= nst && !warp_wait(is_v ? bar_vempty(st) : bar_kempty(st), ((jt / nst) - 1) & 1, wl)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full = is_v ? bar_vfull(st) : bar_kfull(st);
+                    const uint32_t full = vz ? bar_vz : is_v ? bar_vfull(st) : bar_kfull(st);
                     const uint32_t dst = is_v ? v_base(st) : k_base(st);
                     if (lane == 0) mbar_arrive_expect_tx(full, S::KV_BYTES);
     #pragma unroll
@@ -652,22 +655,23 @@ __global__ void __launch_bounds__(kPrefillThreads<T, TC>, 1)
                             for (int dh = 0; dh < S::DH; ++dh)
                                 tc05::tma_load_2d(dst + dh * S::KV_HALF + bi * BS * 128, map, dh * 64, row, full);
                     }
-                    // the item's last key tile: V rows from the context end to the end
-                    // of its last block hold whatever the pool holds there
-                    if (is_v && t == nT - 1 && it.vz_r0 < it.vz_r1) {
-                        if (vz_jt >= 0) do_vz();
+                    if (vz) {
                         vz_jt = jt;
                         vz_r0 = it.vz_r0;
                         vz_r1 = it.vz_r1;
                     }
                 }
             }
-            if (is_v && vz_jt >= 0 && ok) do_vz();
+            if (vz_jt >= 0 && ok) do_vz();
             if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_WAIT);
             if (lane == 0) {
                 // every copy requested above lands before this warp leaves (the last
                 // copy into each stage; earlier ones were consumed before their stage
-                // was refilled)
+                // was refilled); a tile that is still pending completes its stage as it is
+                if (vz_jt >= 0) {
+                    mbar_wait_bounded(bar_vz, vz_n & 1, kWaitLimit);
+                    mbar_arrive(bar_vfull(vz_jt % VST));
+                }
                 for (int t = max(0, jt - nst); t < jt; ++t)
                     mbar_wait_bounded(is_v ? bar_vfull(t % nst) : bar_kfull(t % nst), (t / nst) & 1, kWaitLimit);
             }
