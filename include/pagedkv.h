@@ -232,12 +232,15 @@ pkv_status reshape_and_cache_fp8kv(const void* key, const void* value, void* k_c
  *
  * paged_attention_decode_fp8row: paged_attention_decode over such caches.  The
  * softmax weights are taken relative to the largest weight times V scale, so
- * rows of very different scales keep their precision.  With 16-bit q the
- * products run on the tensor cores in fp16; bf16 q goes in times a power
- * of two as over the per-tensor cache.  With 16-bit q, G >= 17, scale > 0 and partition_size 0
- * the call takes the tcgen05 kernel, in q's type: weights are rounded to it,
- * and elements are taken in it as in paged_attention_prefill_fp8row.
- * Workspace, partitioning, checks and errors as for paged_attention_decode.
+ * rows of very different scales keep their precision (one whose weight is below
+ * 2^-126 of that drops out).  With 16-bit q the products run on the tensor cores
+ * in fp16; bf16 q goes in times a power of two as over the per-tensor cache.
+ * With 16-bit q, G >= 17, scale > 0 and partition_size 0 the call takes the tcgen05
+ * kernel, in q's type: weights are rounded to it, and elements are taken in it as
+ * in paged_attention_prefill_fp8row (so with f16 q and such groups what is beyond
+ * +-65504 is not what smaller groups make of it).
+ * Workspace, checks and errors as for paged_attention_decode, its partitions too but
+ * that for G < 4 the library's choice is 192 tokens (256 in blocks of 32).
  *
  * Scale bytes the calls never write (below 67, 188 to 254) give undefined
  * values, and codes 0x7f / 0xff occur only in NaN rows.
@@ -376,8 +379,9 @@ size_t paged_attention_workspace_size(int num_seqs, int num_heads, int num_kv_he
 
 /* The smallest partition size paged_attention_decode may use for these
  * arguments: the requested size, or for partition_size 0 the lower end of
- * the library's range (the kernel then picks, per call, a block multiple
- * between this and twice this that keeps the last round of work items full).
+ * the library's range (the kernel then picks, per call, a block multiple from
+ * there on that keeps the last round of work items full).  Not for 8-bit row caches:
+ * see paged_attention_decode_fp8row.
  * Contexts up to this length are never split.  0 on bad arguments. */
 int paged_attention_partition_size(int num_heads, int num_kv_heads, int block_size,
                                    int max_context_len, int partition_size);
@@ -562,9 +566,10 @@ pkv_status paged_attention_prefill(void* out, const void* q, const void* k_cache
  * with those formats.  Each cache element is taken in q's type: exact in bf16
  * and within fp16's range; with f16 q an element of a row cache beyond +-65504
  * (an f16 element from 63488 on is such a one: it was stored as 65536) counts as
- * +-65504 in K and as an infinity in V, and one below 2^-21 may be rounded, to a multiple of 2^-24.  Here NaN
- * and infinite elements reach the queries that see their token and no others:
- * an infinity of V makes its dim of the output infinite, both signs NaN. */
+ * +-65504 in K and as an infinity in V, and one below 2^-21 may be rounded, to a
+ * multiple of 2^-24.  Here NaN and infinite elements of V reach the queries that
+ * see their token and no others: an infinity makes its dim of the output infinite,
+ * both signs NaN. */
 pkv_status paged_attention_prefill_fp8kv(void* out, const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables, const int32_t* context_lens,
                                          const int32_t* query_start_loc, float scale, float k_scale, float v_scale,

@@ -12,8 +12,10 @@
 // Quantising a row x: e is the smallest exponent in [-60, 60] with max|x| <=
 // 448 * 2^e; codes are x * 2^-e rounded once, to nearest even, saturating at
 // +-448; b = e + 127.  The clamp keeps every product of scales and softmax
-// weights inside fp32's range.  A row that holds a NaN gets b = 255 and NaN
-// codes: it reads as NaN throughout.
+// weights below fp32's largest; a weight below 2^-126 beside the largest
+// contribution counts as none, also in the sum (that takes V scales 2^100 apart in
+// one context).  A row that holds a NaN gets b = 255 and NaN codes: it reads as NaN
+// throughout.
 #pragma once
 
 #include "common.cuh"

@@ -301,8 +301,8 @@ pkv_status decode_impl(void* out, const void* q, const void* k_cache, const void
     // fp32 q over row caches: the fp32 consumer's work bounds the call, and is the
     // same for all slices of a group together, so a call with fewer items than
     // warps takes narrower ones: 43 sequences of 237-403 tokens, 8 heads over one
-    // KV head, 34 us with 1 column and 162 with 8; but 300 of 500-4000 with 64 heads
-    // over 8, 2263 and 1371.  (The kernels of 1 and 2 columns take whole groups
+    // KV head, 34 us with 1 column and 85 with 8; but 300 of 500-4000 with 64 heads
+    // over 8, 2294 and 1289.  (The kernels of 1 and 2 columns take whole groups
     // of that size only.)
     if (kind == pkv::CacheKind::kFp8Row && dtype == PKV_F32)
         while (G > 1 && (int64_t)num_seqs * wl.max_parts * num_kv_heads * ((Greal + G - 1) / G) < (int64_t)12 * sms)
