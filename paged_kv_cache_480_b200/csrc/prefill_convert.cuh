@@ -273,7 +273,7 @@ struct SliceConverter {
                     c = make_uint4(0u, 0u, 0u, 0u);
                     b = 127;
                 }
-                if (aside.at && (kRow ? b > P::FAST : has_nan_code(c)))
+                if (aside.at && (kRow ? b > (P::kHalf ? P::FAST : kRowScaleMax) : has_nan_code(c)))
                     take_out<T, D>(c, b, aside, aside.t0 + r0 + u, (int)(src - (r0 / BS) * TILE) % D);
                 const bool in = b >= P::LO && b <= P::HI;
                 uint4 lo, hi;

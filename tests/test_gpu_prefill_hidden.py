@@ -158,3 +158,22 @@ def test_k_elements_from_the_end_of_fp16_in_decode(D, bs, G):
         K, V = (rm.sequence(c, bs, D, bt, s, L) for c in (kc, vc))
         ref, logit, top = masked_reference(q[s:s + 1], K, V, 1e-5, torch.float16)
         rm.close(out[s:s + 1], ref, rm.attention_bound(ref, logit, top, torch.float16, torch.float16, L) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D,bs,G", [(64, 16, 1), (128, 32, 4)])
+def test_v_rows_of_large_scales(dt, D, bs, G):
+    """Every 50th row 2^8 to 2^50 times as large: bf16 holds all of it, of fp16 a row
+    has elements on both sides of its range."""
+    def large(x, g):
+        x = x.clone()
+        n = x[20::50].shape[0]
+        x[20::50] *= torch.exp2(torch.randint(8, 51, (n, x.shape[1], 1), generator=g, device="cuda").float())
+        if n:
+            x[20::50, :, ::3] *= 2.0 ** -16
+        return x
+    lens, counts, Hkv = [300, 40, 130], [300, 40, 90], 2
+    kc, vc, bt, cl, gc = paged_rows(lens, Hkv * G, Hkv, D, bs, dt, 76, vscale=large)
+    q = torch.randn(sum(counts), Hkv * G, D, generator=gc, device="cuda").to(rm.DT[dt])
+    check("paged_attention_prefill_fp8row", lens, counts, Hkv * G, D, bs, dt, kc, vc, bt,
+          lambda c, s, L: rm.sequence(c, bs, D, bt, s, L), q, D ** -0.5)
